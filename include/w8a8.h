@@ -54,7 +54,8 @@ typedef enum {
   W8A8_ERR_OUT_DTYPE = 5, /* unknown output type                         */
   W8A8_ERR_ALIAS = 6,     /* an output overlaps an input or other output */
   W8A8_ERR_DEVICE = 7,    /* no HIP device, or it is not gfx950          */
-  W8A8_ERR_HIP = 8        /* a HIP call or kernel launch failed          */
+  W8A8_ERR_HIP = 8,       /* a HIP call or kernel launch failed          */
+  W8A8_ERR_ARG = 9        /* an option is unknown or out of range        */
 } w8a8_status_t;
 
 /* Largest K accepted by w8a8_gemm / w8a8_linear: with INT8 operands every
@@ -278,6 +279,161 @@ int w8a8_pow2_renorm_quantize(const uint16_t *x, int64_t M, int64_t K,
                               void *stream);
 int w8a8_quantize_act_silu(const uint16_t *x, int64_t M, int64_t K,
                            int8_t *a_q, float *a_scale, void *stream);
+
+/*
+ * Block norms: what stands between a block's projections.
+ *
+ * In front of a projection the block normalizes its input row and modulates
+ * it (a shift and a scale per token or per group of tokens); behind the
+ * attention output and the MLP it may normalize the branch, gates it and adds
+ * it to the residual.  With r the residual row after the addition:
+ *
+ *   norm(v)  RMS:    v * rsqrt(mean(v^2) + eps) * weight
+ *            LAYER:  (v - mean(v)) * rsqrt(mean((v - mean(v))^2) + eps)
+ *                    * weight + bias
+ *            NONE:   v
+ *   r = residual_scale * x + gate[i] * post(branch)
+ *   y = pre(r) * (1 + scale[i]) + shift[i]
+ *
+ * all in binary32 (sums and statistics included).  r is rounded to BF16 where
+ * it is written; the norm behind it reads r before that rounding, and the
+ * quantizing forms take y before any rounding to BF16: the scale is
+ * max|y| / 127 and the codes round_half_even(y / scale), each operation as in
+ * w8a8_quantize_act.  (norm_modulate followed by quantize_act quantizes the
+ * rounded y instead, and may differ by a code.)
+ *
+ * i is the token's modulation row: row[m] when `row` is given, else m when
+ * rows == M, else 0 (rows must then be 1).  A row[m] outside [0, rows) marks
+ * token m as padding: its branch row is not read, r is x unchanged bit for
+ * bit, y and its codes and scale are zero.  `row` needs rows >= 1 also where
+ * no vector is given.
+ *
+ * Rows are independent: a row that holds Inf or NaN spoils only itself.
+ * Sums of squares must stay below the binary32 range (|x| below about 2^56).
+ */
+typedef enum {
+  W8A8_NORM_NONE = 0,
+  W8A8_NORM_RMS = 1,
+  W8A8_NORM_LAYER = 2
+} w8a8_norm_kind_t;
+
+typedef struct {
+  int kind;               /* w8a8_norm_kind_t                               */
+  float eps;              /* 2^-126 <= eps < Inf (ignored for NONE)          */
+  const uint16_t *weight; /* BF16 [H], 16-byte aligned, or NULL (ones)       */
+  const uint16_t *bias;   /* BF16 [H], 16-byte aligned, or NULL (zeros);
+                             LAYER only.  NONE takes neither.               */
+} w8a8_norm_t;
+
+/* Modulation vectors: each is NULL (scale and shift 0, gate 1) or `rows` rows
+ * of H BF16 values at its own row stride in elements (so that the parts of
+ * one [rows, 6 H] table can be passed as they are): 16-byte aligned, strides
+ * multiples of 8, H or more and below 2^30, or 0 (one row for all).  The
+ * residual alone reads no scale and shift, the norm alone no gate. */
+typedef struct {
+  const uint16_t *scale, *shift, *gate;
+  int64_t scale_stride, shift_stride, gate_stride;
+  int64_t rows;           /* 1 <= rows < 2^31 (0 without any vector)         */
+  const int32_t *row;     /* int32 [M], 4-byte aligned, or NULL              */
+} w8a8_modulation_t;
+
+/* Largest row the block norms take (it stays in registers). */
+#define W8A8_NORM_MAX_H 32768
+
+/*
+ * w8a8_norm_modulate            x -> y.
+ * w8a8_norm_modulate_quantize   x -> codes and scales of y.
+ * w8a8_gated_residual           x, branch -> r.
+ * w8a8_gated_residual_norm      x, branch -> r, y.
+ * w8a8_gated_residual_norm_quantize
+ *                               x, branch -> r, codes and scales of y.
+ *   x, branch, r, y  BF16 [M,H], 16-byte aligned; r may be x itself (in
+ *             place), no other overlap of an output with anything.
+ *   a_q       INT8 [M,H], 8-byte aligned; a_scale FP32 [M], 4-byte aligned.
+ *   post, pre the norms; NULL means NONE.  mod NULL means no modulation.
+ *   residual_scale  finite.
+ * The structs are read during the call only.
+ * Shape: 1 <= M <= 2^24 - 1, 8 <= H <= W8A8_NORM_MAX_H, H % 8 == 0.
+ * Errors: NULL, SHAPE (M, H, rows, strides), ARG (kind, eps, residual_scale, a
+ * weight or bias that the kind does not take), ALIGN, ALIAS, DEVICE, HIP.
+ */
+int w8a8_norm_modulate(const uint16_t *x, int64_t M, int64_t H,
+                       const w8a8_norm_t *pre, const w8a8_modulation_t *mod,
+                       uint16_t *y, void *stream);
+int w8a8_norm_modulate_quantize(const uint16_t *x, int64_t M, int64_t H,
+                                const w8a8_norm_t *pre,
+                                const w8a8_modulation_t *mod, int8_t *a_q,
+                                float *a_scale, void *stream);
+int w8a8_gated_residual(const uint16_t *x, const uint16_t *branch, int64_t M,
+                        int64_t H, const w8a8_norm_t *post,
+                        const w8a8_modulation_t *mod, float residual_scale,
+                        uint16_t *r, void *stream);
+int w8a8_gated_residual_norm(const uint16_t *x, const uint16_t *branch,
+                             int64_t M, int64_t H, const w8a8_norm_t *post,
+                             const w8a8_norm_t *pre,
+                             const w8a8_modulation_t *mod,
+                             float residual_scale, uint16_t *r, uint16_t *y,
+                             void *stream);
+int w8a8_gated_residual_norm_quantize(
+    const uint16_t *x, const uint16_t *branch, int64_t M, int64_t H,
+    const w8a8_norm_t *post, const w8a8_norm_t *pre,
+    const w8a8_modulation_t *mod, float residual_scale, uint16_t *r,
+    int8_t *a_q, float *a_scale, void *stream);
+
+/*
+ * Linear over few tokens with packed 4-bit weights and group scales.
+ *
+ * A weight is (u - 8) * s, u its 4-bit code and s the BF16 scale of its group:
+ * `group` (32, 64 or 128) consecutive inputs of one output channel.  The
+ * activations stay BF16: y[m,n] = bf16(sum_k x[m,k] * w[n,k] + bias[n]), each
+ * group's sum of x * (u - 8) and the sum over groups in binary32.  At few
+ * tokens the weights are the bytes a Linear moves; half of the INT8 ones.
+ *
+ * Packed layout (N % 16 == 0, K % 128 == 0), written by the two converters
+ * below, contiguous, one block per 16 channels x 128 inputs:
+ *   w4       uint8 [N/16][K/128][64][16]: byte b of lane l holds the codes of
+ *            channel 16 i + l % 16 at input 128 j + 32 (b / 4) + 8 (l / 16) +
+ *            b % 4 (low four bits) and at the input 4 further (high bits);
+ *   w4_scale BF16 [N/16][K/128][16][128/group]: the scale of channel 16 i + c
+ *            for the inputs from 128 j + group * t on.
+ * Any content of w4 is valid.
+ */
+
+/*
+ * Converts a BF16 weight [N,K] in a Linear's layout: per group, scale =
+ * bf16(max|w| / 7) (1 for a group of zeros, at least the smallest BF16 above
+ * zero otherwise) and code = clamp(round_half_even(w / scale), -7, 7), the
+ * divisions in binary32.
+ *   w 16-byte aligned; w4 and w4_scale 16-byte aligned, overlapping nothing.
+ * Shape: 16 <= N < 2^26, N % 16 == 0; 128 <= K <= W8A8_MAX_K, K % 128 == 0;
+ * N * K < 2^37 (a launch holds fewer than 2^32 work-items).  Errors: NULL,
+ * SHAPE, ARG (group), ALIGN, ALIAS, DEVICE, HIP.
+ */
+int w8a8_w4_quantize_weight(const uint16_t *w, int64_t N, int64_t K,
+                            int64_t group, uint8_t *w4, uint16_t *w4_scale,
+                            void *stream);
+
+/*
+ * Packs codes and scales that were made elsewhere: codes INT8 [N,K] (values
+ * outside [-8, 7] are clamped), scales BF16 [N, K/group], both row-major and
+ * 16-byte aligned.  Shape and errors as w8a8_w4_quantize_weight.
+ */
+int w8a8_w4_pack_weight(const int8_t *codes, const uint16_t *scales,
+                        int64_t N, int64_t K, int64_t group, uint8_t *w4,
+                        uint16_t *w4_scale, void *stream);
+
+/*
+ * The product.  x BF16 [M,K] and y BF16 [M,N], 16-byte aligned; w4 and
+ * w4_scale as above; bias BF16 [N], 2-byte aligned, or NULL.  No workspace.
+ * Made for at most 64 tokens: beyond that the weights are read again for
+ * every 64.  Shape: 1 <= M <= 64 * 65535; N and K as above.
+ * Errors: NULL, SHAPE, ARG (group), ALIGN, ALIAS (y overlapping an input),
+ * DEVICE, HIP.
+ */
+int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
+                   const uint16_t *w4_scale, const uint16_t *bias,
+                   uint16_t *y, int64_t M, int64_t N, int64_t K,
+                   int64_t group, void *stream);
 
 #ifdef __cplusplus
 }

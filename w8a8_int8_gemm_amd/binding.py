@@ -20,12 +20,32 @@ STATUS = {
     0: "W8A8_OK", 1: "W8A8_ERR_NULL", 2: "W8A8_ERR_SHAPE",
     3: "W8A8_ERR_ALIGN", 4: "W8A8_ERR_WORKSPACE", 5: "W8A8_ERR_OUT_DTYPE",
     6: "W8A8_ERR_ALIAS", 7: "W8A8_ERR_DEVICE", 8: "W8A8_ERR_HIP",
+    9: "W8A8_ERR_ARG",
 }
 MAX_K = 130944
 GLUE_MAX_K = 90112   # SiLU, renormalization and the fused quantizers
+NORM_MAX_H = 32768   # block norms
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+W4_GROUPS = (32, 64, 128)
+
+
+class _Norm(ctypes.Structure):  # w8a8_norm_t
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class _Modulation(ctypes.Structure):  # w8a8_modulation_t
+    _fields_ = [("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("shift_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("row", ctypes.c_void_p)]
+
 
 # Every symbol include/w8a8.h declares, with its ctypes signature.
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_F = ctypes.c_float
+_PN, _PM = ctypes.POINTER(_Norm), ctypes.POINTER(_Modulation)
 SIGNATURES = {
     "w8a8_quantize_act": (_I, [_P, _I64, _I64, _P, _P, _P]),
     "w8a8_quantize_act_silu": (_I, [_P, _I64, _I64, _P, _P, _P]),
@@ -47,6 +67,17 @@ SIGNATURES = {
     "w8a8_check_scales": (_I, [_P, _I64, _P, _P]),
     "w8a8_swiglu_bf16": (_I, [_P, _P, _I64, _I64, _P]),
     "w8a8_quantize_act_swiglu": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "w8a8_norm_modulate": (_I, [_P, _I64, _I64, _PN, _PM, _P, _P]),
+    "w8a8_norm_modulate_quantize": (_I, [_P, _I64, _I64, _PN, _PM, _P, _P,
+                                         _P]),
+    "w8a8_gated_residual": (_I, [_P, _P, _I64, _I64, _PN, _PM, _F, _P, _P]),
+    "w8a8_gated_residual_norm": (_I, [_P, _P, _I64, _I64, _PN, _PN, _PM, _F,
+                                      _P, _P, _P]),
+    "w8a8_gated_residual_norm_quantize": (_I, [_P, _P, _I64, _I64, _PN, _PN,
+                                               _PM, _F, _P, _P, _P, _P]),
+    "w8a8_w4_quantize_weight": (_I, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "w8a8_w4_pack_weight": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "w8a8_w4_linear": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]),
 }
 
 
@@ -434,3 +465,280 @@ def quantize_act_swiglu(h, *, out=None, stream=None):
     if out is None:
         _on_stream(stream, q, s)
     return q, s
+
+
+# ---------------------------------------------------------------------------
+# block norms
+# ---------------------------------------------------------------------------
+
+def _norm_arg(kind, weight, bias, eps, H, name):
+    """A w8a8_norm_t; the vectors must outlive the call."""
+    torch = _torch()
+    if kind not in NORM_KINDS:
+        raise ValueError(f"{name}: expected one of {sorted(NORM_KINDS)}, got "
+                         f"{kind!r}")
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, torch.bfloat16, 1, f"{name} {what}", (H,))
+    return _Norm(NORM_KINDS[kind], eps,
+                 None if weight is None else weight.data_ptr(),
+                 None if bias is None else bias.data_ptr())
+
+
+def _mod_arg(M, H, mod_row, **vectors):
+    """A w8a8_modulation_t from bf16 vectors [H] or tables [rows, H] (rows at
+    any stride, their values contiguous) that agree on `rows`."""
+    torch = _torch()
+    mod = _Modulation()
+    rows = None
+    for name, t in vectors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if (t.dtype != torch.bfloat16 or t.dim() not in (1, 2) or
+                t.shape[-1] != H or (H > 1 and t.stride(-1) != 1)):
+            raise ValueError(f"{name}: expected {torch.bfloat16} [{H}] or "
+                             f"[rows, {H}] with contiguous rows, got "
+                             f"{t.dtype} {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be on the current GPU "
+                             f"(cuda:{torch.cuda.current_device()})")
+        n = 1 if t.dim() == 1 else t.shape[0]
+        if rows is not None and n != rows:
+            raise ValueError(f"{name}: {n} rows, the other vectors have "
+                             f"{rows}")
+        rows = n
+        setattr(mod, name, t.data_ptr())
+        setattr(mod, name + "_stride", 0 if n == 1 else t.stride(0))
+    if mod_row is not None:
+        _need(mod_row, torch.int32, 1, "mod_row", (M,))
+        mod.row = mod_row.data_ptr()
+    elif rows not in (None, 1, M):
+        raise ValueError(f"{rows} modulation rows for {M} tokens need mod_row")
+    # without vectors mod_row says only which tokens are padding
+    mod.rows = rows if rows is not None else 2**31 - 1 if mod.row else 0
+    return mod
+
+
+def norm_modulate(x, *, norm="rms", weight=None, bias=None, eps=1e-6,
+                  scale=None, shift=None, mod_row=None, out=None,
+                  stream=None):
+    """x: bf16 [M, H] -> bf16 [M, H], norm(x) * (1 + scale) + shift.
+
+    norm: "rms", "layer" or "none"; weight, bias: bf16 [H].  scale, shift:
+    bf16 [H], [M, H], or [rows, H] with mod_row (int32 [M]) naming each
+    token's row; a row outside [0, rows) marks padding (its output is 0)."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, H = x.shape
+    pre = _norm_arg(norm, weight, bias, eps, H, "norm")
+    mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift)
+    y = torch.empty_like(x) if out is None else out
+    _need(y, torch.bfloat16, 2, "out", (M, H))
+    _check("w8a8_norm_modulate", lib().w8a8_norm_modulate(
+        _ptr(x), M, H, pre, mod, _ptr(y), _stream(stream)))
+    if out is None:
+        _on_stream(stream, y)
+    return y
+
+
+def norm_modulate_quantize(x, *, norm="rms", weight=None, bias=None,
+                           eps=1e-6, scale=None, shift=None, mod_row=None,
+                           out=None, stream=None):
+    """norm_modulate and the per-token quantization of its values (taken in
+    binary32, not rounded to BF16 first) in one pass: x bf16 [M, H] ->
+    (a_q int8 [M, H], a_scale float32 [M])."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, H = x.shape
+    pre = _norm_arg(norm, weight, bias, eps, H, "norm")
+    mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift)
+    if out is None:
+        q = torch.empty((M, H), dtype=torch.int8, device=x.device)
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    else:
+        q, s = out
+        _need(q, torch.int8, 2, "out[0]", (M, H))
+        _need(s, torch.float32, 1, "out[1]", (M,))
+    _check("w8a8_norm_modulate_quantize", lib().w8a8_norm_modulate_quantize(
+        _ptr(x), M, H, pre, mod, _ptr(q), _ptr(s), _stream(stream)))
+    if out is None:
+        _on_stream(stream, q, s)
+    return q, s
+
+
+def gated_residual(x, branch, *, gate=None, residual_scale=1.0,
+                   post_norm="none", post_weight=None, post_bias=None,
+                   post_eps=1e-6, mod_row=None, out=None, stream=None):
+    """x, branch: bf16 [M, H] -> bf16 [M, H], residual_scale * x + gate *
+    post_norm(branch).  gate as norm_modulate's scale; a padding token keeps
+    x.  out may be x (in place)."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, H = x.shape
+    _need(branch, torch.bfloat16, 2, "branch", (M, H))
+    post = _norm_arg(post_norm, post_weight, post_bias, post_eps, H,
+                     "post_norm")
+    mod = _mod_arg(M, H, mod_row, gate=gate)
+    r = torch.empty_like(x) if out is None else out
+    _need(r, torch.bfloat16, 2, "out", (M, H))
+    _check("w8a8_gated_residual", lib().w8a8_gated_residual(
+        _ptr(x), _ptr(branch), M, H, post, mod, residual_scale, _ptr(r),
+        _stream(stream)))
+    if out is None:
+        _on_stream(stream, r)
+    return r
+
+
+def gated_residual_norm(x, branch, *, gate=None, residual_scale=1.0,
+                        post_norm="none", post_weight=None, post_bias=None,
+                        post_eps=1e-6, norm="rms", weight=None, bias=None,
+                        eps=1e-6, scale=None, shift=None, mod_row=None,
+                        out=None, stream=None):
+    """gated_residual and the norm_modulate of its sum (before that is
+    rounded to BF16) in one pass -> (r bf16 [M, H], y bf16 [M, H])."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, H = x.shape
+    _need(branch, torch.bfloat16, 2, "branch", (M, H))
+    post = _norm_arg(post_norm, post_weight, post_bias, post_eps, H,
+                     "post_norm")
+    pre = _norm_arg(norm, weight, bias, eps, H, "norm")
+    mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift, gate=gate)
+    if out is None:
+        r, y = torch.empty_like(x), torch.empty_like(x)
+    else:
+        r, y = out
+        _need(r, torch.bfloat16, 2, "out[0]", (M, H))
+        _need(y, torch.bfloat16, 2, "out[1]", (M, H))
+    _check("w8a8_gated_residual_norm", lib().w8a8_gated_residual_norm(
+        _ptr(x), _ptr(branch), M, H, post, pre, mod, residual_scale, _ptr(r),
+        _ptr(y), _stream(stream)))
+    if out is None:
+        _on_stream(stream, r, y)
+    return r, y
+
+
+def gated_residual_norm_quantize(x, branch, *, gate=None, residual_scale=1.0,
+                                 post_norm="none", post_weight=None,
+                                 post_bias=None, post_eps=1e-6, norm="rms",
+                                 weight=None, bias=None, eps=1e-6, scale=None,
+                                 shift=None, mod_row=None, out=None,
+                                 stream=None):
+    """gated_residual and the norm_modulate_quantize of its sum (before that
+    is rounded to BF16) in one pass -> (r bf16 [M, H], a_q int8 [M, H],
+    a_scale float32 [M])."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, H = x.shape
+    _need(branch, torch.bfloat16, 2, "branch", (M, H))
+    post = _norm_arg(post_norm, post_weight, post_bias, post_eps, H,
+                     "post_norm")
+    pre = _norm_arg(norm, weight, bias, eps, H, "norm")
+    mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift, gate=gate)
+    if out is None:
+        r = torch.empty_like(x)
+        q = torch.empty((M, H), dtype=torch.int8, device=x.device)
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    else:
+        r, q, s = out
+        _need(r, torch.bfloat16, 2, "out[0]", (M, H))
+        _need(q, torch.int8, 2, "out[1]", (M, H))
+        _need(s, torch.float32, 1, "out[2]", (M,))
+    _check("w8a8_gated_residual_norm_quantize",
+           lib().w8a8_gated_residual_norm_quantize(
+               _ptr(x), _ptr(branch), M, H, post, pre, mod, residual_scale,
+               _ptr(r), _ptr(q), _ptr(s), _stream(stream)))
+    if out is None:
+        _on_stream(stream, r, q, s)
+    return r, q, s
+
+
+# ---------------------------------------------------------------------------
+# linear over few tokens with packed 4-bit weights
+# ---------------------------------------------------------------------------
+
+def _w4_out(N, K, group, device, out):
+    torch = _torch()
+    if group not in W4_GROUPS:
+        raise ValueError(f"group: expected one of {W4_GROUPS}, got {group}")
+    if N % 16 or K % 128 or not N or not K:
+        raise ValueError(f"a packed 4-bit weight needs N % 16 == 0 and "
+                         f"K % 128 == 0, got {N} x {K}")
+    shapes = ((N // 16, K // 128, 64, 16),
+              (N // 16, K // 128, 16, 128 // group))
+    if out is None:
+        return (torch.empty(shapes[0], dtype=torch.uint8, device=device),
+                torch.empty(shapes[1], dtype=torch.bfloat16, device=device))
+    w4, s = out
+    _need(w4, torch.uint8, 4, "out[0]", shapes[0])
+    _need(s, torch.bfloat16, 4, "out[1]", shapes[1])
+    return w4, s
+
+
+def w4_quantize_weight(w, *, group=128, out=None, stream=None):
+    """w: bf16 [N, K] -> (w4 uint8 [N/16, K/128, 64, 16], w4_scale bf16
+    [N/16, K/128, 16, 128/group]): 4-bit codes with one scale per `group`
+    (32, 64 or 128) inputs of a channel, packed for w4_linear."""
+    torch = _torch()
+    _need(w, torch.bfloat16, 2, "w")
+    N, K = w.shape
+    w4, s = _w4_out(N, K, group, w.device, out)
+    _check("w8a8_w4_quantize_weight", lib().w8a8_w4_quantize_weight(
+        _ptr(w), N, K, group, _ptr(w4), _ptr(s), _stream(stream)))
+    if out is None:
+        _on_stream(stream, w4, s)
+    return w4, s
+
+
+def w4_pack_weight(codes, scales, *, out=None, stream=None):
+    """Codes int8 [N, K] (clamped to [-8, 7]) and scales bf16 [N, K/group]
+    made elsewhere -> (w4, w4_scale) as w4_quantize_weight."""
+    torch = _torch()
+    _need(codes, torch.int8, 2, "codes")
+    N, K = codes.shape
+    _need(scales, torch.bfloat16, 2, "scales")
+    if scales.shape[0] != N or not scales.shape[1] or K % scales.shape[1]:
+        raise ValueError(f"scales: expected [{N}, K/group], got "
+                         f"{tuple(scales.shape)}")
+    group = K // scales.shape[1]
+    w4, s = _w4_out(N, K, group, codes.device, out)
+    _check("w8a8_w4_pack_weight", lib().w8a8_w4_pack_weight(
+        _ptr(codes), _ptr(scales), N, K, group, _ptr(w4), _ptr(s),
+        _stream(stream)))
+    if out is None:
+        _on_stream(stream, w4, s)
+    return w4, s
+
+
+def w4_linear(x, w4, w4_scale, bias=None, *, out=None, stream=None):
+    """x: bf16 [M, K], a packed 4-bit weight -> bf16 [M, N], x . w^T + bias
+    (weight-only: x stays BF16).  Made for at most 64 tokens."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, K = x.shape
+    _need(w4, torch.uint8, 4, "w4")
+    if tuple(w4.shape[1:]) != (K // 128, 64, 16) or K % 128:
+        raise ValueError(f"w4: expected [N/16, {K}/128, 64, 16], got "
+                         f"{tuple(w4.shape)}")
+    N = 16 * w4.shape[0]
+    _need(w4_scale, torch.bfloat16, 4, "w4_scale")
+    if (tuple(w4_scale.shape[:3]) != (*w4.shape[:2], 16) or
+            w4_scale.shape[3] not in (1, 2, 4)):
+        raise ValueError(f"w4_scale: expected [{w4.shape[0]}, {w4.shape[1]}, "
+                         f"16, 128/group], got {tuple(w4_scale.shape)}")
+    if bias is not None:
+        _need(bias, torch.bfloat16, 1, "bias", (N,))
+    own_out = out is None
+    if own_out:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, torch.bfloat16, 2, "out", (M, N))
+    _check("w8a8_w4_linear", lib().w8a8_w4_linear(
+        _ptr(x), _ptr(w4), _ptr(w4_scale), _ptr(bias), _ptr(out), M, N, K,
+        128 // w4_scale.shape[3], _stream(stream)))
+    _on_stream(stream, out if own_out else None)
+    return out

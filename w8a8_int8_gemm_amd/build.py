@@ -23,9 +23,10 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libw8a8.so"
-SOURCES = ["w8a8_api.cpp", "rowwise.hip", "gemm.hip"]
+SOURCES = ["w8a8_api.cpp", "rowwise.hip", "gemm.hip", "norm.hip", "w4.hip"]
 # Headers the library's sources include (part of its build id).
-HEADERS = [CSRC / "internal.h", CSRC / "rowwise.h", ROOT / "include" / "w8a8.h"]
+HEADERS = [CSRC / "internal.h", CSRC / "rowwise.h", CSRC / "quant.h",
+           CSRC / "norm.h", CSRC / "w4.h", ROOT / "include" / "w8a8.h"]
 # Measurement support, not part of the library: the register-only MFMA
 # rate on given code matrices (loaded by bench.py only).
 CEILING_LIB = PKG / "libw8a8_ceiling.so"

@@ -6,12 +6,16 @@
 // caller's stream.  The library allocates nothing and never synchronizes.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <unordered_map>
 
 #include "internal.h"
+#include "norm.h"
 #include "rowwise.h"
+#include "w4.h"
 #include "w8a8.h"
 
 namespace {
@@ -168,6 +172,139 @@ int validate_gemm(const int8_t *a_q, const float *a_scale, const int8_t *w_q,
                        out, out_dtype, M, N, K);
 }
 
+// One norm of a block-norm call: its kind and constants.
+int validate_norm(const w8a8_norm_t *n) {
+  if (!n || n->kind == W8A8_NORM_NONE)
+    return n && (n->weight || n->bias) ? W8A8_ERR_ARG : W8A8_OK;
+  if (n->kind != W8A8_NORM_RMS && n->kind != W8A8_NORM_LAYER)
+    return W8A8_ERR_ARG;
+  if (!(n->eps >= FLT_MIN) || !std::isfinite(n->eps)) return W8A8_ERR_ARG;
+  if (n->bias && n->kind != W8A8_NORM_LAYER) return W8A8_ERR_ARG;
+  if ((n->weight && !aligned(n->weight, 16)) ||
+      (n->bias && !aligned(n->bias, 16)))
+    return W8A8_ERR_ALIGN;
+  return W8A8_OK;
+}
+
+// Row strides of a modulation table: the bytes of 2^31 rows stay below 2^63.
+constexpr int64_t kMaxModStride = int64_t(1) << 30;
+
+// Bytes a modulation table spans, or -1 for a stride the contract rejects.
+int64_t mod_bytes(int64_t stride, int64_t rows, int64_t H) {
+  if (stride != 0 && (stride < H || stride % 8 != 0 || stride >= kMaxModStride))
+    return -1;
+  return ((rows - 1) * stride + H) * 2;
+}
+
+// The block norms: everything is checked here, `a` filled in and the kernel
+// launched.  Which outputs there are says what is computed.
+int block_norm(const uint16_t *x, const uint16_t *branch, int64_t M,
+               int64_t H, const w8a8_norm_t *post, const w8a8_norm_t *pre,
+               const w8a8_modulation_t *mod, float residual_scale,
+               uint16_t *r, uint16_t *y, int8_t *q, float *qs, void *stream) {
+  if (M < 1 || M > kMaxTokenRows || H < 8 || H % 8 != 0 ||
+      H > W8A8_NORM_MAX_H)
+    return W8A8_ERR_SHAPE;
+  int st = validate_norm(post);
+  if (st == W8A8_OK) st = validate_norm(pre);
+  if (st != W8A8_OK) return st;
+  if (!std::isfinite(residual_scale)) return W8A8_ERR_ARG;
+  w8a8::NormArgs a{};
+  if (mod) {
+    const bool any = mod->scale || mod->shift || mod->gate || mod->row;
+    if (any ? mod->rows < 1 || mod->rows > kMaxRows : mod->rows < 0)
+      return W8A8_ERR_SHAPE;
+    if (any && !mod->row && mod->rows != 1 && mod->rows != M)
+      return W8A8_ERR_SHAPE;
+    if (mod->row && !aligned(mod->row, 4)) return W8A8_ERR_ALIGN;
+    a.scale = mod->scale;
+    a.shift = mod->shift;
+    a.gate = mod->gate;
+    a.scale_stride = mod->scale_stride;
+    a.shift_stride = mod->shift_stride;
+    a.gate_stride = mod->gate_stride;
+    a.row = mod->row;
+    a.rows = any ? (int)mod->rows : 1;
+    a.row_step = any && !mod->row && mod->rows > 1 ? 1 : 0;
+  } else {
+    a.rows = 1;
+  }
+  // Inputs besides x and branch, with their sizes in bytes.
+  const void *in[8];
+  int64_t in_bytes[8];
+  int n_in = 0;
+  const uint16_t *vec[3] = {a.scale, a.shift, a.gate};
+  const int64_t stride[3] = {a.scale_stride, a.shift_stride, a.gate_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (!vec[i]) continue;
+    const int64_t bytes = mod_bytes(stride[i], a.rows, H);
+    if (bytes < 0) return W8A8_ERR_SHAPE;
+    if (!aligned(vec[i], 16)) return W8A8_ERR_ALIGN;
+    in[n_in] = vec[i];
+    in_bytes[n_in++] = bytes;
+  }
+  if (a.row) {
+    in[n_in] = a.row;
+    in_bytes[n_in++] = M * 4;
+  }
+  if (post) {
+    a.post_kind = post->kind;
+    a.post_eps = post->eps;
+    a.post_weight = post->weight;
+    a.post_bias = post->bias;
+  }
+  if (pre) {
+    a.kind = pre->kind;
+    a.eps = pre->eps;
+    a.weight = pre->weight;
+    a.bias = pre->bias;
+  }
+  for (const uint16_t *w : {a.post_weight, a.post_bias, a.weight, a.bias}) {
+    if (!w) continue;
+    in[n_in] = w;
+    in_bytes[n_in++] = H * 2;
+  }
+  if (!aligned(x, 16) || !aligned(branch, 16) || !aligned(r, 16) ||
+      !aligned(y, 16) || !aligned(q, 8) || !aligned(qs, 4))
+    return W8A8_ERR_ALIGN;
+  const Range rx = range_of(x, M * H * 2),
+              rb = range_of(branch, branch ? M * H * 2 : 0);
+  const Range out[4] = {range_of(r, r ? M * H * 2 : 0),
+                        range_of(y, y ? M * H * 2 : 0),
+                        range_of(q, q ? M * H : 0),
+                        range_of(qs, qs ? M * 4 : 0)};
+  for (int i = 0; i < 4; ++i) {
+    if (!(i == 0 && r == x) && overlap(out[i], rx)) return W8A8_ERR_ALIAS;
+    if (overlap(out[i], rb)) return W8A8_ERR_ALIAS;
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i], range_of(in[j], in_bytes[j])))
+        return W8A8_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return W8A8_ERR_ALIAS;
+  }
+  if ((st = check_device()) != W8A8_OK) return st;
+  a.x = x;
+  a.branch = branch;
+  a.r = r;
+  a.y = y;
+  a.q = q;
+  a.qs = qs;
+  a.M = M;
+  a.H = (int)H;
+  a.residual_scale = residual_scale;
+  return hip_status(
+      w8a8::launch_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+// Shape and group of a packed 4-bit weight.
+int validate_w4(int64_t N, int64_t K, int64_t group) {
+  if (N < 16 || N % 16 != 0 || N >= (int64_t(1) << 26) || K < 128 ||
+      K % 128 != 0 || K > W8A8_MAX_K || N * K >= (int64_t(1) << 37))
+    return W8A8_ERR_SHAPE;
+  if (group != 32 && group != 64 && group != 128) return W8A8_ERR_ARG;
+  return W8A8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -183,6 +320,7 @@ const char *w8a8_status_string(int status) {
     case W8A8_ERR_ALIAS: return "an output overlaps another buffer";
     case W8A8_ERR_DEVICE: return "no HIP device, or it is not gfx950";
     case W8A8_ERR_HIP: return "a HIP call or kernel launch failed";
+    case W8A8_ERR_ARG: return "an option is unknown or out of range";
     default: return "unknown status";
   }
 }
@@ -405,6 +543,114 @@ int w8a8_pow2_renorm_quantize(const uint16_t *x, int64_t M, int64_t K,
   if (st != W8A8_OK) return st;
   return hip_status(w8a8::launch_pow2_renorm_quant(
       x, y, a_q, a_scale, M, K, static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_norm_modulate(const uint16_t *x, int64_t M, int64_t H,
+                       const w8a8_norm_t *pre, const w8a8_modulation_t *mod,
+                       uint16_t *y, void *stream) {
+  if (!x || !y) return W8A8_ERR_NULL;
+  return block_norm(x, nullptr, M, H, nullptr, pre, mod, 1.0f, nullptr, y,
+                    nullptr, nullptr, stream);
+}
+
+int w8a8_norm_modulate_quantize(const uint16_t *x, int64_t M, int64_t H,
+                                const w8a8_norm_t *pre,
+                                const w8a8_modulation_t *mod, int8_t *a_q,
+                                float *a_scale, void *stream) {
+  if (!x || !a_q || !a_scale) return W8A8_ERR_NULL;
+  return block_norm(x, nullptr, M, H, nullptr, pre, mod, 1.0f, nullptr,
+                    nullptr, a_q, a_scale, stream);
+}
+
+int w8a8_gated_residual(const uint16_t *x, const uint16_t *branch, int64_t M,
+                        int64_t H, const w8a8_norm_t *post,
+                        const w8a8_modulation_t *mod, float residual_scale,
+                        uint16_t *r, void *stream) {
+  if (!x || !branch || !r) return W8A8_ERR_NULL;
+  return block_norm(x, branch, M, H, post, nullptr, mod, residual_scale, r,
+                    nullptr, nullptr, nullptr, stream);
+}
+
+int w8a8_gated_residual_norm(const uint16_t *x, const uint16_t *branch,
+                             int64_t M, int64_t H, const w8a8_norm_t *post,
+                             const w8a8_norm_t *pre,
+                             const w8a8_modulation_t *mod,
+                             float residual_scale, uint16_t *r, uint16_t *y,
+                             void *stream) {
+  if (!x || !branch || !r || !y) return W8A8_ERR_NULL;
+  return block_norm(x, branch, M, H, post, pre, mod, residual_scale, r, y,
+                    nullptr, nullptr, stream);
+}
+
+int w8a8_gated_residual_norm_quantize(
+    const uint16_t *x, const uint16_t *branch, int64_t M, int64_t H,
+    const w8a8_norm_t *post, const w8a8_norm_t *pre,
+    const w8a8_modulation_t *mod, float residual_scale, uint16_t *r,
+    int8_t *a_q, float *a_scale, void *stream) {
+  if (!x || !branch || !r || !a_q || !a_scale) return W8A8_ERR_NULL;
+  return block_norm(x, branch, M, H, post, pre, mod, residual_scale, r,
+                    nullptr, a_q, a_scale, stream);
+}
+
+int w8a8_w4_quantize_weight(const uint16_t *w, int64_t N, int64_t K,
+                            int64_t group, uint8_t *w4, uint16_t *w4_scale,
+                            void *stream) {
+  if (!w || !w4 || !w4_scale) return W8A8_ERR_NULL;
+  int st = validate_w4(N, K, group);
+  if (st != W8A8_OK) return st;
+  if (!aligned(w, 16) || !aligned(w4, 16) || !aligned(w4_scale, 16))
+    return W8A8_ERR_ALIGN;
+  const Range rw = range_of(w, N * K * 2), rq = range_of(w4, N * K / 2),
+              rs = range_of(w4_scale, N * K / group * 2);
+  if (overlap(rw, rq) || overlap(rw, rs) || overlap(rq, rs))
+    return W8A8_ERR_ALIAS;
+  if ((st = check_device()) != W8A8_OK) return st;
+  return hip_status(w8a8::launch_w4_quantize(
+      w, N, K, (int)group, w4, w4_scale, static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_w4_pack_weight(const int8_t *codes, const uint16_t *scales,
+                        int64_t N, int64_t K, int64_t group, uint8_t *w4,
+                        uint16_t *w4_scale, void *stream) {
+  if (!codes || !scales || !w4 || !w4_scale) return W8A8_ERR_NULL;
+  int st = validate_w4(N, K, group);
+  if (st != W8A8_OK) return st;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(w4, 16) ||
+      !aligned(w4_scale, 16))
+    return W8A8_ERR_ALIGN;
+  const int64_t sb = N * K / group * 2;
+  const Range rc = range_of(codes, N * K), rs = range_of(scales, sb),
+              rq = range_of(w4, N * K / 2), ro = range_of(w4_scale, sb);
+  if (overlap(rc, rq) || overlap(rc, ro) || overlap(rs, rq) ||
+      overlap(rs, ro) || overlap(rq, ro))
+    return W8A8_ERR_ALIAS;
+  if ((st = check_device()) != W8A8_OK) return st;
+  return hip_status(
+      w8a8::launch_w4_pack(codes, scales, N, K, (int)group, w4, w4_scale,
+                           static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
+                   const uint16_t *w4_scale, const uint16_t *bias,
+                   uint16_t *y, int64_t M, int64_t N, int64_t K,
+                   int64_t group, void *stream) {
+  if (!x || !w4 || !w4_scale || !y) return W8A8_ERR_NULL;
+  if (M < 1 || M > 64 * 65535) return W8A8_ERR_SHAPE;
+  int st = validate_w4(N, K, group);
+  if (st != W8A8_OK) return st;
+  if (!aligned(x, 16) || !aligned(w4, 16) || !aligned(w4_scale, 16) ||
+      !aligned(y, 16) || !aligned(bias, 2))
+    return W8A8_ERR_ALIGN;
+  const Range ry = range_of(y, M * N * 2);
+  const Range ins[] = {range_of(x, M * K * 2), range_of(w4, N * K / 2),
+                       range_of(w4_scale, N * K / group * 2),
+                       range_of(bias, bias ? N * 2 : 0)};
+  for (const Range &r : ins)
+    if (overlap(ry, r)) return W8A8_ERR_ALIAS;
+  if ((st = check_device()) != W8A8_OK) return st;
+  return hip_status(w8a8::launch_w4_linear(
+      x, w4, w4_scale, bias, y, M, N, K, (int)group,
+      static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
