@@ -298,9 +298,11 @@ int w8a8_quantize_act_silu(const uint16_t *x, int64_t M, int64_t K,
  * all in binary32 (sums and statistics included).  r is rounded to BF16 where
  * it is written; the norm behind it reads r before that rounding, and the
  * quantizing forms take y before any rounding to BF16: the scale is
- * max|y| / 127 and the codes round_half_even(y / scale), each operation as in
- * w8a8_quantize_act.  (norm_modulate followed by quantize_act quantizes the
- * rounded y instead, and may differ by a code.)
+ * max|y| / 127 and the codes are the integers nearest to y / scale in [-127,
+ * 127] (taken as y times the reciprocal: either neighbour where y / scale lies
+ * within 2^-15 of a half; a row of zeros has scale 0 and codes 0).
+ * (norm_modulate followed by quantize_act quantizes the rounded y instead, and
+ * may differ by a code.)
  *
  * i is the token's modulation row: row[m] when `row` is given, else m when
  * rows == M, else 0 (rows must then be 1).  A row[m] outside [0, rows) marks
@@ -309,7 +311,8 @@ int w8a8_quantize_act_silu(const uint16_t *x, int64_t M, int64_t K,
  * no vector is given.
  *
  * Rows are independent: a row that holds Inf or NaN spoils only itself.
- * Sums of squares must stay below the binary32 range (|x| below about 2^56).
+ * Sums of squares must stay below the binary32 range (|x| below about 2^56);
+ * behind an RMS or layer norm a row that breaks this has a NaN scale.
  */
 typedef enum {
   W8A8_NORM_NONE = 0,
@@ -353,7 +356,8 @@ typedef struct {
  *   post, pre the norms; NULL means NONE.  mod NULL means no modulation.
  *   residual_scale  finite.
  * The structs are read during the call only.
- * Shape: 1 <= M <= 2^24 - 1, 8 <= H <= W8A8_NORM_MAX_H, H % 8 == 0.
+ * Shape: 1 <= M <= 2^24 - 1, 8 <= H <= W8A8_NORM_MAX_H, H % 8 == 0,
+ * M * H < 2^36.
  * Errors: NULL, SHAPE (M, H, rows, strides), ARG (kind, eps, residual_scale, a
  * weight or bias that the kind does not take), ALIGN, ALIAS, DEVICE, HIP.
  */

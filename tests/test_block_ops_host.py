@@ -83,6 +83,7 @@ def test_valid_calls_reach_the_device_check(which):
     (dict(x=None), NULL), (dict(M=0), SHAPE), (dict(M=-1), SHAPE),
     (dict(M=1 << 24), SHAPE), (dict(H=0), SHAPE), (dict(H=4), SHAPE),
     (dict(H=1020), SHAPE), (dict(H=32776), SHAPE),
+    (dict(M=(1 << 24) - 1, H=4104, mod=None), SHAPE),
     (dict(x=P["x"] + 8), ALIGN),
     (dict(mod=mod(rows=0)), SHAPE), (dict(mod=mod(rows=-1)), SHAPE),
     (dict(mod=mod(rows=1 << 31)), SHAPE),

@@ -166,6 +166,28 @@ def test_tokens(M):
         run_case(M, 136, M, quantize, branch=False, norm="rms", mods="token")
 
 
+@pytest.mark.parametrize("H,M", [
+    (8, 250001), (512, 12001), (520, 12001), (1000, 6001), (1536, 4001),
+    (1544, 4001), (3064, 2001), (5376, 1201), (8192, 801), (12288, 601),
+    (16384, 401), (24576, 301), (24584, 301), (32768, 201)])
+def test_many_values(H, M):
+    """Past the size where work groups take two rows: odd row counts, runs of
+    equal modulation rows, changes inside a pair, padding, one row each."""
+    say(f"norm many H={H} M={M}")
+    for quantize in (False, True):
+        for mods in ("index", "token", "broadcast"):
+            x, kw = inputs(M, H, H + M, post="rms", norm="layer", mods=mods,
+                           padded=mods == "index")
+            if mods == "index":
+                row = (torch.arange(M, device="cuda") // 7 % 5).to(torch.int32)
+                row[M // 2::5] = -1
+                kw["mod_row"] = row
+            verify(x, kw, quantize, call(x, kw, quantize))
+            if mods != "token":
+                x, kw = inputs(M, H, H, branch=False, norm="rms", mods=mods)
+                verify(x, kw, quantize, call(x, kw, quantize))
+
+
 @pytest.mark.parametrize("H", [136, 5376])
 @pytest.mark.parametrize("quantize", [False, True])
 def test_padding_rows(H, quantize):
@@ -228,6 +250,29 @@ def test_special_rows():
             assert got[0][7].isnan().all()
     y = call(x, {"norm_kind": "rms"})
     assert y[7].isnan().all() and y[8].isnan().any()
+    for kind in ("rms", "layer"):
+        s = call(x, {"norm_kind": kind}, True)[1]
+        assert s[[7, 8]].isnan().all() and s[fine].isfinite().all()
+
+
+def test_scales_down_to_subnormal():
+    """Rows whose code scale is tiny, subnormal, or rounds to zero, through
+    the map of one value to codes (no norm)."""
+    H = 256
+    base = rand(gen(2), 40, H).float()
+    base[:, 0] = 4.0
+    x = (base * 2.0 ** -torch.arange(90, 130, device="cuda").float()[:, None]
+         ).to(BF)
+    x[39, :] = 0
+    x[39, :3] = 2.0 ** -133
+    q, s = B.norm_modulate_quantize(x, norm="none")
+    amax = x.double().abs().amax(1)
+    assert ((s.double() - amax / 127).abs() <=
+            amax / 127 * 2.0 ** -23 + 2.0 ** -150).all()
+    v = x.double() / torch.where(s == 0, 1.0, s)[:, None].double()
+    off = (q.double() - v.clamp(-127, 127)).abs()
+    assert (off <= torch.where(s == 0, 1.0, 0.5 + 2.0 ** -14)[:, None]).all()
+    assert (q[s == 0] == 0).all() and (q >= -127).all()
 
 
 @pytest.mark.parametrize("eps", [2.0**-126, 1e-12, 1e-5, 10.0])

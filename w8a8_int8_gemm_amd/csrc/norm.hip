@@ -6,18 +6,17 @@
 // Bound by HBM: 4 bytes a value for a norm to BF16, 3 to codes, 8 and 7 with
 // the residual part; a dozen binary32 operations a value.  A row is read once
 // and stays in registers through all of its reductions.
+//
+// A work group owns R consecutive rows, so that the vectors of a modulation row
+// that they share are read, unpacked and joined once.
 #include "internal.h"
 #include "norm.h"
-#include "quant.h"
 #include "w8a8.h"
 
 namespace w8a8 {
 namespace {
 
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
-
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 
 enum NormOut : int { OUT_NONE = 0, OUT_ROW = 1, OUT_CODES = 2 };
 
@@ -36,18 +35,27 @@ __device__ __forceinline__ F8 unpack8(v4u c) {
   return f;
 }
 
+// Keeps the compiler from holding a packed row's 32-bit values from one pass
+// over it to the next: twice the registers, where unpacking again costs one
+// operation a value.
+template <int CH>
+__device__ __forceinline__ void forget(v4u (&c)[CH]) {
+#pragma unroll
+  for (int i = 0; i < CH; ++i) asm volatile("" : "+v"(c[i]));
+}
+
 __device__ __forceinline__ v4u pack8(const F8 &f) {
   return v4u{pack_bf16x2(f.v[0], f.v[1]), pack_bf16x2(f.v[2], f.v[3]),
              pack_bf16x2(f.v[4], f.v[5]), pack_bf16x2(f.v[6], f.v[7])};
 }
 
-// Chunk j (8 values) of a vector, or eight times `absent`.
-__device__ __forceinline__ F8 vec8(const uint16_t *p, int j, float absent) {
-  if (p) return unpack8(reinterpret_cast<const v4u *>(p)[j]);
-  F8 f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f.v[e] = absent;
-  return f;
+// Chunk j (8 values) of a vector; where there is none, pairs of `absent`.
+constexpr uint32_t kZeros = 0, kOnes = 0x3F803F80u;
+
+__device__ __forceinline__ v4u vec8(const uint16_t *p, uint32_t j,
+                                    uint32_t absent) {
+  return p ? reinterpret_cast<const v4u *>(p)[j]
+           : v4u{absent, absent, absent, absent};
 }
 
 template <bool MAX>
@@ -55,179 +63,464 @@ __device__ __forceinline__ float join(float a, float b) {
   return MAX ? fmaxf(a, b) : a + b;
 }
 
-// Sum or maximum over the work group; `part` holds kWaves values and is free
-// for the next call after the barrier at its start.
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float *part) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1)
-    v = join<MAX>(v, __shfl_xor(v, off, 64));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) v = join<MAX>(v, part[w]);
-  return v;
+template <bool MAX, int CTRL>
+__device__ __forceinline__ float join_dpp(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF,
+                                            0xF, true);
+  return join<MAX>(v, __int_as_float(o));
 }
 
-// Normalizes the row held in v in place, without weight and bias: the mean
-// first, then the squares of the differences, so that a large mean costs the
-// variance no digits.  Values past the row's end are zero and stay unused.
-template <int CH>
-__device__ __forceinline__ void normalize(F8 (&v)[CH], int kind, float eps,
-                                          int H, float *part) {
-  const int chunks = H >> 3;
+// Sum or maximum over a row of 16 lanes: within quads, halves and the row by
+// lane permutations of the adder's own operand.
+template <bool MAX>
+__device__ __forceinline__ float row16_reduce(float v) {
+  v = join_dpp<MAX, 0xB1>(v);      // lane ^ 1
+  v = join_dpp<MAX, 0x4E>(v);      // lane ^ 2
+  v = join_dpp<MAX, 0x141>(v);     // mirrored within 8
+  return join_dpp<MAX, 0x140>(v);  // mirrored within 16
+}
+
+template <bool MAX>
+__device__ __forceinline__ float wave_reduce(float v) {
+  const int b = __float_as_int(row16_reduce<MAX>(v));
+  const float r0 = __int_as_float(__builtin_amdgcn_readlane(b, 0)),
+              r1 = __int_as_float(__builtin_amdgcn_readlane(b, 16)),
+              r2 = __int_as_float(__builtin_amdgcn_readlane(b, 32)),
+              r3 = __int_as_float(__builtin_amdgcn_readlane(b, 48));
+  return join<MAX>(join<MAX>(r0, r1), join<MAX>(r2, r3));
+}
+
+// Sums or maxima (of values >= 0) of R rows over the waves of a work group.
+// Two slots are used in turn: a slot is written again only after every wave
+// has passed the barrier of the reduction between, and so has read it.  Places
+// of waves that the group does not have hold zero.
+constexpr int kMaxWaves = 16;
+
+template <int R>
+struct Reducer {
+  float (*part)[R][kMaxWaves];
+  int slot;
+
+  __device__ __forceinline__ void clear() {
+    float *p = &part[0][0][0];
+    for (int i = threadIdx.x; i < 2 * R * kMaxWaves; i += blockDim.x)
+      p[i] = 0.0f;
+    __syncthreads();
+  }
+
+  template <bool MAX>
+  __device__ __forceinline__ void reduce(float (&v)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = wave_reduce<MAX>(v[r]);
+    if (blockDim.x == 64) return;
+    float(*p)[kMaxWaves] = part[slot];
+    slot ^= 1;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r) p[r][threadIdx.x >> 6] = v[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      v[r] = row16_reduce<MAX>(p[r][threadIdx.x & 15]);
+  }
+};
+
+// A row's statistics as the map v -> v * f + c that normalizes it: f =
+// 1 / sqrt(mean square + eps), c = -mean * f.  The mean first, then the squares
+// of the differences, so that a large mean costs the variance no digits.
+struct Stats {
+  float f, c;
+};
+
+// `Row` gives chunk i of row r (CH chunks a thread, thread t of `step`; places
+// past the row's end are zero) as 8 values, `squares` adds those of chunk i,
+// `again` stands between two passes.
+template <int R, int CH, class Row, class Squares, class Again>
+__device__ __forceinline__ void row_stats(Stats (&st)[R], int kind, float eps,
+                                          int t, int step, int chunks,
+                                          float inv_h, Reducer<R> &red,
+                                          Row row, Squares squares,
+                                          Again again) {
+  float sq[R], mean[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    st[r] = Stats{1.0f, 0.0f};
+    sq[r] = mean[r] = 0.0f;
+  }
   if (kind == W8A8_NORM_NONE) return;
   if (kind == W8A8_NORM_LAYER) {
-    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += v[i].v[e];
-    const float mean = block_reduce<false>(sum, part) / (float)H;
+      for (int i = 0; i < CH; ++i) {
+        const F8 v = row(r, i);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const bool ok = i * kThreads + (int)threadIdx.x < chunks;
+        for (int e = 0; e < 8; ++e) mean[r] += v.v[e];
+      }
+    red.template reduce<false>(mean);
+    again();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i].v[e] = ok ? v[i].v[e] - mean : 0.0f;
-    }
-  }
-  float sq = 0.0f;
+    for (int r = 0; r < R; ++r) {
+      mean[r] *= inv_h;
 #pragma unroll
-  for (int i = 0; i < CH; ++i)
+      for (int i = 0; i < CH; ++i) {
+        const F8 v = row(r, i);
+        const float mi = i * step + t < chunks ? mean[r] : 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq = fmaf(v[i].v[e], v[i].v[e], sq);
-  const float rs =
-      rsqrtf(block_reduce<false>(sq, part) / (float)H + eps);
-#pragma unroll
-  for (int i = 0; i < CH; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[i].v[e] *= rs;
-}
-
-template <int CH, bool RES, int OUT>
-__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
-  __shared__ float part[kWaves];
-  const int64_t m = blockIdx.x;
-  const int t = threadIdx.x;
-  const int chunks = a.H >> 3;
-  const int64_t at = m * (int64_t)a.H;
-  const v4u *xr = reinterpret_cast<const v4u *>(a.x + at);
-  const int64_t mr = a.row ? (int64_t)a.row[m] : m * a.row_step;
-
-  if (mr < 0 || mr >= a.rows) {  // padding: r = x, the rest zero
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int j = i * kThreads + t;
-      if (j >= chunks) continue;
-      if (RES && a.r != a.x) reinterpret_cast<v4u *>(a.r + at)[j] = xr[j];
-      if (OUT == OUT_ROW) reinterpret_cast<v4u *>(a.y + at)[j] = v4u{0, 0, 0, 0};
-      if (OUT == OUT_CODES)
-        reinterpret_cast<uint2 *>(a.q + at)[j] = make_uint2(0, 0);
-    }
-    if (OUT == OUT_CODES && t == 0) a.qs[m] = 0.0f;
-    return;
-  }
-
-  F8 v[CH];
-  if (RES) {
-    const v4u *br = reinterpret_cast<const v4u *>(a.branch + at);
-    const uint16_t *gate = a.gate ? a.gate + mr * a.gate_stride : nullptr;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int j = i * kThreads + t;
-      v[i] = unpack8(j < chunks ? br[j] : v4u{0, 0, 0, 0});
-    }
-    normalize<CH>(v, a.post_kind, a.post_eps, a.H, part);
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int j = i * kThreads + t;
-      if (j >= chunks) continue;
-      const F8 x = unpack8(xr[j]);
-      const F8 w = vec8(a.post_weight, j, 1.0f);
-      const F8 b = vec8(a.post_bias, j, 0.0f);
-      const F8 g = vec8(gate, j, 1.0f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[i].v[e] = fmaf(g.v[e], fmaf(v[i].v[e], w.v[e], b.v[e]),
-                         a.residual_scale * x.v[e]);
-      reinterpret_cast<v4u *>(a.r + at)[j] = pack8(v[i]);
+        for (int e = 0; e < 8; ++e) {
+          const float d = v.v[e] - mi;
+          sq[r] = fmaf(d, d, sq[r]);
+        }
+      }
     }
   } else {
 #pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) sq[r] = squares(r, i, sq[r]);
+  }
+  red.template reduce<false>(sq);
+  again();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    st[r].f = rsqrtf(sq[r] * inv_h + eps);
+    st[r].c = -mean[r] * st[r].f;
+  }
+}
+
+// sq plus the squares of 8 packed values: products exact, two to an addition.
+__device__ __forceinline__ float squares8(v4u c, float sq) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const bf2v p = __builtin_bit_cast(bf2v, w[e]);
+    sq = __builtin_amdgcn_fdot2_f32_bf16(p, p, sq, false);
+  }
+  return sq;
+}
+
+__device__ __forceinline__ float squares8(const F8 &v, float sq) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sq = fmaf(v.v[e], v.v[e], sq);
+  return sq;
+}
+
+// The map n -> n * a + b of a normalized value, for 8 channels.
+struct Affine {
+  F8 a, b;
+};
+
+// What a map is made of, for a chunk: the vectors of modulation row mr and the
+// norm's weight.  The bias, which few norms have, is read where it is used.
+struct PostVecs {
+  v4u gate, weight;
+};
+
+__device__ __forceinline__ PostVecs post_vecs(const NormArgs &a, int64_t mr,
+                                              uint32_t j) {
+  return PostVecs{
+      vec8(a.gate ? a.gate + mr * a.gate_stride : nullptr, j, kOnes),
+      vec8(a.post_weight, j, kOnes)};
+}
+
+// gate behind the post-norm's weight and bias.
+__device__ __forceinline__ Affine post_map(const NormArgs &a,
+                                           const PostVecs &p, uint32_t j) {
+  const F8 g = unpack8(p.gate), w = unpack8(p.weight);
+  Affine f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f.a.v[e] = g.v[e] * w.v[e];
+    f.b.v[e] = 0.0f;
+  }
+  if (a.post_bias) {
+    const F8 b = unpack8(vec8(a.post_bias, j, kZeros));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.b.v[e] = g.v[e] * b.v[e];
+  }
+  return f;
+}
+
+struct PreVecs {
+  v4u scale, shift, weight;
+};
+
+__device__ __forceinline__ PreVecs pre_vecs(const NormArgs &a, int64_t mr,
+                                            uint32_t j) {
+  return PreVecs{
+      vec8(a.scale ? a.scale + mr * a.scale_stride : nullptr, j, kZeros),
+      vec8(a.shift ? a.shift + mr * a.shift_stride : nullptr, j, kZeros),
+      vec8(a.weight, j, kOnes)};
+}
+
+// 1 + scale and shift behind the norm's weight and bias.
+__device__ __forceinline__ Affine pre_map(const NormArgs &a, const PreVecs &p,
+                                          uint32_t j) {
+  const F8 s = unpack8(p.scale), w = unpack8(p.weight);
+  Affine f;
+  f.b = unpack8(p.shift);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    f.a.v[e] = fmaf(w.v[e], s.v[e], w.v[e]);  // w (1 + s), rounded once
+  if (a.bias) {
+    const F8 b = unpack8(vec8(a.bias, j, kZeros));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f.b.v[e] += fmaf(b.v[e], s.v[e], b.v[e]);
+  }
+  return f;
+}
+
+// Scale and reciprocal of a row whose largest magnitude is amax.  The codes
+// are the nearest integers to y * (1 / s): those of y / s but where that lies
+// within 2^-15 of a half (y itself is known no better: the reciprocal is off
+// by 2^-23 and the product by 2^-24 of at most 127, the sum by 2^-17).
+struct CodeRow {
+  float s, r;
+};
+
+// At a scale below 2^-100 the reciprocal could overflow: row and scale are
+// then taken 2^64 times larger.
+constexpr float kSmallScale = 0x1p-100f, kLift = 0x1p64f;
+
+// A row whose factor f is not above zero held Inf, NaN or values whose squares
+// overflow; its scale says so (NaN).
+__device__ __forceinline__ CodeRow code_row(float amax, float f) {
+  const float s = f > 0.0f ? amax / 127.0f : __builtin_nanf("");
+  const float r = __builtin_amdgcn_rcpf(s < kSmallScale ? s * kLift : s);
+  // the same in every lane: keep it in scalar registers
+  return CodeRow{
+      __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(s))),
+      __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(r)))};
+}
+
+// Biased codes of 8 values.  A subnormal scale is so coarse that y / s may pass
+// 127; the conversion clamps above, the maximum below.
+template <bool SMALL>
+__device__ __forceinline__ uint2 codes8(const F8 &y, float r) {
+  uint32_t o[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float u = SMALL ? fmaxf(fmaf(y.v[e] * kLift, r, 128.0f), 1.0f)
+                          : fmaf(y.v[e], r, 128.0f);
+    o[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(u, e % 4, o[e / 4]);
+  }
+  // biased bytes -> two's complement codes
+  return make_uint2(o[0] ^ 0x80808080u, o[1] ^ 0x80808080u);
+}
+
+__device__ __forceinline__ uint2 codes8(const F8 &y, const CodeRow &c) {
+  if (c.s >= kSmallScale) return codes8<false>(y, c.r);
+  if (c.s == 0.0f) return make_uint2(0, 0);
+  return codes8<true>(y, c.r);
+}
+
+// The R rows from blockIdx.x * R on; a thread holds chunks t, t + step, ... of
+// each.  Registers set the pace once memory does not: a form that walks a long
+// run of rows with the vectors kept and the next rows loaded ahead holds more
+// of them and ran 14 to 50% slower; one wave a row without barriers spilled.
+template <int R, int CH, bool RES, int OUT>
+__global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
+  __shared__ float part[2][R][kMaxWaves];
+  Reducer<R> red{part, 0};
+  const int t = threadIdx.x, step = blockDim.x;
+  const int chunks = a.H >> 3;
+  const float inv_h = 1.0f / (float)a.H;
+  const int64_t m0 = (int64_t)blockIdx.x * R;
+  // chunk j of row m0 + r
+  auto chunk = [&](const void *p, int r, uint32_t j) {
+    return reinterpret_cast<const v4u *>(p) + (m0 + r) * (int64_t)chunks + j;
+  };
+
+  // Many rows pass by once and would push the vectors, and what the next
+  // kernel reads, out of the caches (norm to BF16 of 19077 x 5376 85 us, 79
+  // with nontemporal loads; both with codes 143 us, 131 with r stored so too);
+  // a few were written just before and are read soon.
+  auto fetch = [](const v4u *p) {
+    return R > 1 ? __builtin_nontemporal_load(p) : *p;
+  };
+  // Rows past the last one read it again and write nothing.
+  v4u x[R][CH], b[R][CH];
+  int64_t mr[R];
+  bool live[R], same = true;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int rr = (int)min((int64_t)r, a.M - 1 - m0);
+    mr[r] = a.row ? (int64_t)a.row[m0 + rr] : (m0 + rr) * a.row_step;
+    live[r] = mr[r] >= 0 && mr[r] < a.rows;
+    same = same && live[r] && mr[r] == mr[0];
+#pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int j = i * kThreads + t;
-      v[i] = unpack8(j < chunks ? xr[j] : v4u{0, 0, 0, 0});
+      const int j = i * step + t;
+      x[r][i] = j < chunks ? fetch(chunk(a.x, rr, j)) : v4u{0, 0, 0, 0};
+      if (RES)
+        b[r][i] = j < chunks ? fetch(chunk(a.branch, rr, j)) : v4u{0, 0, 0, 0};
+    }
+  }
+  red.clear();
+  auto forget = [&](v4u (&c)[R][CH]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) w8a8::forget<CH>(c[r]);
+  };
+  auto in_range = [&](int r) { return R == 1 || m0 + r < a.M; };
+
+  // The vectors of the maps are on their way while a reduction goes on (read
+  // behind it: norm to codes of 37503 x 5376 150 us, so 128).
+  F8 v[R][CH];  // the residual rows, or the output on its way to codes
+  Stats st[R];
+  PreVecs pv[CH];
+  auto load_pre = [&]() {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (same && i * step + t < chunks)
+        pv[i] = pre_vecs(a, mr[0], i * step + t);
+  };
+  if (RES) {
+    PostVecs gv[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (same && i * step + t < chunks)
+        gv[i] = post_vecs(a, mr[0], i * step + t);
+    row_stats<R, CH>(
+        st, a.post_kind, a.post_eps, t, step, chunks, inv_h, red,
+        [&](int r, int i) { return unpack8(b[r][i]); },
+        [&](int r, int i, float sq) { return squares8(b[r][i], sq); },
+        [&]() { forget(b); });
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = i * step + t;
+#pragma unroll
+      for (int r = 0; r < R; ++r) v[r][i] = unpack8(v4u{0, 0, 0, 0});
+      if (j >= chunks) continue;
+      Affine g;
+      if (same) g = post_map(a, gv[i], j);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        v4u o = x[r][i];
+        if (live[r]) {
+          if (!same) g = post_map(a, post_vecs(a, mr[r], j), j);
+          const F8 xi = unpack8(x[r][i]), bi = unpack8(b[r][i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[r][i].v[e] = fmaf(fmaf(bi.v[e], st[r].f, st[r].c), g.a.v[e],
+                                fmaf(a.residual_scale, xi.v[e], g.b.v[e]));
+          o = pack8(v[r][i]);
+        }
+        v4u *to = const_cast<v4u *>(chunk(a.r, r, j));
+        if (R > 1 && in_range(r))
+          __builtin_nontemporal_store(o, to);
+        else if (in_range(r))
+          *to = o;
+      }
     }
   }
   if (OUT == OUT_NONE) return;
-
-  normalize<CH>(v, a.kind, a.eps, a.H, part);
-  const uint16_t *scale = a.scale ? a.scale + mr * a.scale_stride : nullptr;
-  const uint16_t *shift = a.shift ? a.shift + mr * a.shift_stride : nullptr;
-  float amax = 0.0f;
+  load_pre();
+  row_stats<R, CH>(
+      st, a.kind, a.eps, t, step, chunks, inv_h, red,
+      [&](int r, int i) { return RES ? v[r][i] : unpack8(x[r][i]); },
+      [&](int r, int i, float sq) {
+        return RES ? squares8(v[r][i], sq) : squares8(x[r][i], sq);
+      },
+      [&]() {
+        if (!RES) forget(x);
+      });
+  float amax[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) amax[r] = 0.0f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int j = i * kThreads + t;
+    const int j = i * step + t;
     if (j >= chunks) continue;
-    const F8 w = vec8(a.weight, j, 1.0f);
-    const F8 b = vec8(a.bias, j, 0.0f);
-    const F8 sc = vec8(scale, j, 0.0f);
-    const F8 sh = vec8(shift, j, 0.0f);
+    Affine g;
+    if (same) g = pre_map(a, pv[i], j);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float n = fmaf(v[i].v[e], w.v[e], b.v[e]);
-      v[i].v[e] = fmaf(n, 1.0f + sc.v[e], sh.v[e]);
-      amax = fmaxf(amax, fabsf(v[i].v[e]));
+    for (int r = 0; r < R; ++r) {
+      F8 y = unpack8(v4u{0, 0, 0, 0});
+      if (live[r]) {
+        if (!same) g = pre_map(a, pre_vecs(a, mr[r], j), j);
+        if (!RES) v[r][i] = unpack8(x[r][i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y.v[e] = fmaf(fmaf(v[r][i].v[e], st[r].f, st[r].c), g.a.v[e],
+                        g.b.v[e]);
+          if (OUT == OUT_CODES) amax[r] = fmaxf(amax[r], fabsf(y.v[e]));
+        }
+      }
+      if (OUT == OUT_CODES) v[r][i] = y;
+      if (OUT == OUT_ROW && in_range(r))
+        *const_cast<v4u *>(chunk(a.y, r, j)) = pack8(y);
     }
-    if (OUT == OUT_ROW) reinterpret_cast<v4u *>(a.y + at)[j] = pack8(v[i]);
   }
   if (OUT != OUT_CODES) return;
-  const QuantRow R = quant_row(block_reduce<true>(amax, part));
-  if (t == 0) a.qs[m] = R.s;
+  red.template reduce<true>(amax);
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int j = i * kThreads + t;
-    if (j >= chunks) continue;
-    uint2 o = make_uint2(0, 0);
-    if (R.s != 0.0f)
-      o = make_uint2(quant4_f32(v[i].v, R), quant4_f32(v[i].v + 4, R));
-    reinterpret_cast<uint2 *>(a.q + at)[j] = o;
+  for (int r = 0; r < R; ++r) {
+    if (!in_range(r)) continue;
+    const CodeRow Q = code_row(amax[r], live[r] ? st[r].f : 1.0f);
+    if (t == 0) a.qs[m0 + r] = Q.s;
+    uint2 *q = reinterpret_cast<uint2 *>(a.q) + (m0 + r) * (int64_t)chunks;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const uint32_t j = i * step + t;
+      if (j < (uint32_t)chunks) q[j] = codes8(v[r][i], Q);
+    }
   }
 }
 
-template <int CH>
-void launch_ch(const NormArgs &a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.M), block(kThreads);
+template <int R, int CH>
+void launch_rows(const NormArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.M + R - 1) / R));
+  const dim3 block(64 * ((a.H / 8 + 64 * CH - 1) / (64 * CH)));
+#define W8A8_NORM_LAUNCH(RES, OUT)                                            \
+  hipLaunchKernelGGL((norm_kernel<R, CH, RES, OUT>), grid, block, 0, stream, a)
   if (a.branch) {
     if (a.q)
-      hipLaunchKernelGGL((norm_kernel<CH, true, OUT_CODES>), grid, block, 0,
-                         stream, a);
+      W8A8_NORM_LAUNCH(true, OUT_CODES);
     else if (a.y)
-      hipLaunchKernelGGL((norm_kernel<CH, true, OUT_ROW>), grid, block, 0,
-                         stream, a);
+      W8A8_NORM_LAUNCH(true, OUT_ROW);
     else
-      hipLaunchKernelGGL((norm_kernel<CH, true, OUT_NONE>), grid, block, 0,
-                         stream, a);
+      W8A8_NORM_LAUNCH(true, OUT_NONE);
   } else if (a.q) {
-    hipLaunchKernelGGL((norm_kernel<CH, false, OUT_CODES>), grid, block, 0,
-                       stream, a);
+    W8A8_NORM_LAUNCH(false, OUT_CODES);
   } else {
-    hipLaunchKernelGGL((norm_kernel<CH, false, OUT_ROW>), grid, block, 0,
-                       stream, a);
+    W8A8_NORM_LAUNCH(false, OUT_ROW);
   }
+#undef W8A8_NORM_LAUNCH
 }
 
 }  // namespace
 
+// R rows a work group, CH chunks a thread, by the values of the call (M * H):
+//  * below 2M values a launch is latency: one chunk a thread (5376 wide, norm
+//    to BF16 and both norms to codes: 64 rows 2.6 and 4.9 us, with three
+//    chunks 3.1 and 5.7; 256 rows 3.7 and 6.2 against 4.1 and 7.1);
+//  * below 6M two chunks, so that a wave's own instructions (addresses,
+//    reductions) weigh less (1024 rows 7.0 and 12.4 us; one chunk 7.6 and
+//    15.1, three and two rows 7.4 and 12.5);
+//  * above, three chunks and two rows that share their vectors (8192 rows 35.0
+//    and 66.6 us; one row 36.5 and 75.7, one chunk 45.9 and 100);
+//  * modulation rows that are each read once have nothing to share: one row
+//    (16384 rows, layer norm to codes 120 us, two rows 133).
+// Waves are as few as that allows, and then the chunks as few as those waves
+// need.  Rows wider than 24576 take four chunks and one row.
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
-  const int ch = (a.H / 8 + kThreads - 1) / kThreads;  // 16 at the largest H
-  if (ch <= 1) launch_ch<1>(a, stream);
-  else if (ch <= 2) launch_ch<2>(a, stream);
-  else if (ch <= 4) launch_ch<4>(a, stream);
-  else if (ch <= 8) launch_ch<8>(a, stream);
-  else if (ch <= 16) launch_ch<16>(a, stream);
+  const int chunks = a.H / 8;
+  const int64_t values = a.M * a.H;
+  const bool many = values >= 6000000;
+  const bool share = !(a.row == nullptr && a.row_step == 1);
+  const int want = values < 2000000 ? 1 : many ? 3 : 2;
+  int waves = (chunks + 64 * want - 1) / (64 * want);
+  if (waves > kMaxWaves) waves = kMaxWaves;
+  const int ch = (chunks + 64 * waves - 1) / (64 * waves);
+  const bool two = many && share;
+  if (ch == 1 && two) launch_rows<2, 1>(a, stream);
+  else if (ch == 1) launch_rows<1, 1>(a, stream);
+  else if (ch == 2 && two) launch_rows<2, 2>(a, stream);
+  else if (ch == 2) launch_rows<1, 2>(a, stream);
+  else if (ch == 3 && two) launch_rows<2, 3>(a, stream);
+  else if (ch == 3) launch_rows<1, 3>(a, stream);
+  else if (ch == 4) launch_rows<1, 4>(a, stream);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

@@ -202,8 +202,10 @@ int block_norm(const uint16_t *x, const uint16_t *branch, int64_t M,
                int64_t H, const w8a8_norm_t *post, const w8a8_norm_t *pre,
                const w8a8_modulation_t *mod, float residual_scale,
                uint16_t *r, uint16_t *y, int8_t *q, float *qs, void *stream) {
+  // With up to 24 values a thread and at least 64 threads a row, fewer than
+  // 2^36 values keep a launch below 2^32 work-items.
   if (M < 1 || M > kMaxTokenRows || H < 8 || H % 8 != 0 ||
-      H > W8A8_NORM_MAX_H)
+      H > W8A8_NORM_MAX_H || M * H >= (int64_t(1) << 36))
     return W8A8_ERR_SHAPE;
   int st = validate_norm(post);
   if (st == W8A8_OK) st = validate_norm(pre);
