@@ -203,7 +203,7 @@ def test_w4_own_rejects():
     assert w4("pack", s4=P["scale"]) == ALIAS
     assert w4("linear", x=None) == NULL
     assert w4("linear", y=None) == NULL
-    for M in (0, -1, 64 * 65535 + 1):
+    for M in (0, -1, 32 * 65535 + 1):
         assert w4("linear", M=M) == SHAPE
     assert w4("linear", x=P["x"] + 8) == ALIGN
     assert w4("linear", y=P["y"] + 8) == ALIGN
@@ -218,7 +218,7 @@ def test_w4_valid_calls_reach_the_device_check():
         for G in B.W4_GROUPS:
             assert w4(which, G=G) == DEVICE
         assert w4(which, N=16, K=B.MAX_K) == DEVICE
-    assert w4("linear", bias=None, M=64 * 65535) == DEVICE
+    assert w4("linear", bias=None, M=32 * 65535) == DEVICE
     assert w4("linear", bias=P["bias"] + 2) == DEVICE
 
 

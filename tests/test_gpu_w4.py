@@ -139,6 +139,47 @@ def test_linear_exact(M, G):
         assert torch.equal(y, want.float().to(BF)), (N, K)
 
 
+@pytest.mark.parametrize("M", [1, 4, 5, 8, 9, 16, 17, 33, 64])
+@pytest.mark.parametrize("tiles", [255, 257, 511, 515, 1021, 1027, 1533, 1543,
+                                   1800])
+def test_linear_exact_wide(M, tiles):
+    """Every number of channel tiles a work group takes, the last group with
+    fewer; K of fewer blocks than waves and of one more round."""
+    say(f"w4 wide M={M} tiles={tiles}")
+    for K, G in ((128, 32), (2176, 128)):
+        N = 16 * tiles
+        g = gen(M * tiles + K)
+        codes, _ = codes_scales(N, K, G, M + N)
+        scales = torch.exp2(torch.randint(-3, 2, (N, K // G), generator=g,
+                                          device="cuda").float()).to(BF)
+        x = torch.randint(-3, 4, (M, K), generator=g, device="cuda").to(BF)
+        w4, s = B.w4_pack_weight(codes, scales)
+        raw = torch.full((M * N * 2 + 8192,), 0xA5, dtype=torch.uint8,
+                         device="cuda")
+        bias = torch.randint(-64, 65, (N,), generator=g, device="cuda").to(BF)
+        y = B.w4_linear(x, w4, s, out=raw[4096:-4096].view(BF).view(M, N))
+        want = x.double() @ weight(codes, scales).t().contiguous()
+        assert torch.equal(y, want.float().to(BF))
+        assert torch.equal(B.w4_linear(x, w4, s, bias),
+                           (want + bias.double()).float().to(BF))
+        assert (raw[:4096] == 0xA5).all() and (raw[-4096:] == 0xA5).all()
+
+
+def test_linear_tiny_inputs():
+    """Inputs below the normal range of BF16, raised by the scales: products
+    and the offset's sum keep them."""
+    N, K = 32, 256
+    codes, scales = codes_scales(N, K, 128, 5)
+    scales[:] = 2.0 ** 100
+    x = (torch.randint(-3, 4, (19, K), generator=gen(2), device="cuda").double()
+         * 2.0 ** -132).to(BF)
+    w4, s = B.w4_pack_weight(codes, scales)
+    for M in (3, 19):
+        want = x[:M].double() @ weight(codes, scales).t().contiguous()
+        assert torch.equal(B.w4_linear(x[:M].contiguous(), w4, s),
+                           want.float().to(BF))
+
+
 def test_linear_every_weight():
     """One-hot tokens read every weight of the layout on its own."""
     N, K = 80, 256

@@ -716,7 +716,7 @@ def w4_pack_weight(codes, scales, *, out=None, stream=None):
 
 def w4_linear(x, w4, w4_scale, bias=None, *, out=None, stream=None):
     """x: bf16 [M, K], a packed 4-bit weight -> bf16 [M, N], x . w^T + bias
-    (weight-only: x stays BF16).  Made for at most 64 tokens."""
+    (weight-only: x stays BF16).  Made for a few tokens."""
     torch = _torch()
     _need(x, torch.bfloat16, 2, "x")
     M, K = x.shape

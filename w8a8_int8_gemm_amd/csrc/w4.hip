@@ -20,6 +20,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 // A packed block: 16 channels x 128 inputs, 16 bytes a lane.
 constexpr int kBlockN = 16, kBlockK = 128, kBlockBytes = 1024;
+constexpr int kCUs = 256;
 
 // ---------------------------------------------------------------------------
 // converters: one wave per block, each lane writing its own 16 bytes
@@ -148,25 +149,118 @@ __device__ __forceinline__ v4f mfma(v4u a, v8bf b, v4f c) {
       __builtin_bit_cast(v8bf, a), b, c, 0, 0, 0);
 }
 
-// A work group owns 16 T channels and up to 16 F tokens; its W waves take the
-// K blocks in turn and join their sums through LDS.  Lane (r, q) of a fragment
-// holds token r (A) or channel r (B) at inputs 8 q .. 8 q + 7 of 32, and
-// results i = 0..3 of token 4 q + i and channel r.
+// The scales of a channel's groups in a block: 128 / G BF16 values.
+template <int G>
+struct Scales;
+template <>
+struct Scales<128> {
+  typedef uint16_t raw;
+  static __device__ __forceinline__ float get(raw r, int) {
+    return bf16_to_f32(r);
+  }
+};
+template <>
+struct Scales<64> {
+  typedef uint32_t raw;
+  static __device__ __forceinline__ float get(raw r, int g) {
+    return g ? __uint_as_float(r & 0xFFFF0000u) : __uint_as_float(r << 16);
+  }
+};
+template <>
+struct Scales<32> {
+  typedef uint2 raw;
+  static __device__ __forceinline__ float get(raw r, int g) {
+    return Scales<64>::get(g < 2 ? r.x : r.y, g & 1);
+  }
+};
+
+// A work group owns 16 T channels and up to 16 F tokens; its waves take the K
+// blocks in turn and join their sums through LDS, so that a launch has waves
+// enough for the weight stream where N is small, and nothing leaves the group.
+// Lane (r, q) of a fragment holds token r (A) or channel r (B) at inputs
+// 8 q .. 8 q + 7 of 32, and results i = 0..3 of token 4 q + i and channel r.
 //
 // The -8 of every code: its products with x do not depend on the channel, so
 // per group they are summed once (B = -8) and are where each channel's sum
 // starts.
-template <int F, int T, int W, int G>
-__global__ __launch_bounds__(W * 64) void w4_linear_kernel(
-    const uint16_t *x, const uint8_t *w4, const uint16_t *scale,
-    const uint16_t *bias, uint16_t *y, int64_t M, int tiles, int kblocks) {
+//
+// x costs more than the weights here: every group reads all of it, and a
+// fragment is 16 rows of 64 bytes.  Taken as fragments from memory it held up
+// the weights (8 tokens, 21504 x 5376: 19.3 us, without x 14.2); as whole rows
+// of 256 bytes turned in LDS, and over T channels' tiles, 15.9 us.
+struct LinearArgs {
+  const uint16_t *x;
+  const uint8_t *w4;
+  const uint16_t *scale, *bias;
+  uint16_t *y;
+  int64_t M;
+  int tiles, kblocks;
+};
+
+// A wave's LDS accesses run in order; this keeps the compiler from moving them
+// past each other where lanes exchange values.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// XR: loads of four rows that x takes (4 F, or fewer where the tokens are).
+template <int F, int XR, int T, int WMAX, int G>
+__global__ __launch_bounds__(WMAX * 64) void w4_linear_kernel(LinearArgs p) {
   constexpr int GPB = kBlockK / G;  // groups a block
-  __shared__ v4f red[W][F][T][64];
+  constexpr int J = 4 / GPB;        // matrix steps a group
+  constexpr int kWaveLds = F * (T > 4 ? T : 4) * 64;  // 16-byte units a wave
+  __shared__ v4f smem[WMAX * kWaveLds];
+  __shared__ float bias_of[16 * T];
+  const int W = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile0 = blockIdx.x * T;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * F);
-  const int64_t K = (int64_t)kblocks * kBlockK, N = (int64_t)tiles * kBlockN;
+  const int M = (int)min(p.M - m0, (int64_t)(16 * F));
+  const int64_t K = (int64_t)p.kblocks * kBlockK;
+  const int64_t N = (int64_t)p.tiles * kBlockN;
+
+  // Uniform bases and 32-bit lane offsets.
+  const uint8_t *wp[T];
+  const uint16_t *sp[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t blk = (int64_t)min(tile0 + t, p.tiles - 1) * p.kblocks;
+    wp[t] = p.w4 + blk * kBlockBytes;
+    sp[t] = p.scale + blk * (kBlockN * GPB);
+  }
+  // x of a block comes as whole rows of 256 bytes, four rows an instruction
+  // (lane l: row l / 16, chunk l % 16), and turns into fragments through this
+  // wave's own piece of LDS: row r keeps chunk c at c ^ r, so that the reads of
+  // 16 rows meet no bank twice.  Rows past the last token read it again or are
+  // zero; their results are not written.
+  v4f *mine = smem + wave * kWaveLds;
+  v4u *xs = reinterpret_cast<v4u *>(mine);
+  uint32_t xo[XR];
+#pragma unroll
+  for (int i = 0; i < XR; ++i)
+    xo[i] = (uint32_t)(min(4 * i + q, M - 1) * K) * 2 + 16 * r;
+  struct Block {
+    v4u w[T];
+    typename Scales<G>::raw s[T];
+    v4u x[XR];
+  };
+  auto load = [&](Block &k, int b) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      k.w[t] = *reinterpret_cast<const v4u *>(
+          wp[t] + (int64_t)b * kBlockBytes + (uint32_t)lane * 16);
+      k.s[t] = *(reinterpret_cast<const typename Scales<G>::raw *>(
+                     sp[t] + (int64_t)b * (kBlockN * GPB)) +
+                 (uint32_t)r);
+    }
+    const char *xb =
+        reinterpret_cast<const char *>(p.x + m0 * K + (int64_t)b * kBlockK);
+#pragma unroll
+    for (int i = 0; i < XR; ++i)
+      k.x[i] = *reinterpret_cast<const v4u *>(xb + xo[i]);
+  };
 
   v8bf minus8;
 #pragma unroll
@@ -176,89 +270,91 @@ __global__ __launch_bounds__(W * 64) void w4_linear_kernel(
   for (int f = 0; f < F; ++f)
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[f][t] = v4f{0, 0, 0, 0};
-
-  for (int b = wave; b < kblocks; b += W) {
-    v4u wv[T];
-    float sc[T][GPB];
+  auto multiply = [&](const Block &k) {
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int64_t blk = (int64_t)min(tile0 + t, tiles - 1) * kblocks + b;
-      wv[t] = reinterpret_cast<const v4u *>(w4 + blk * kBlockBytes)[lane];
-#pragma unroll
-      for (int g = 0; g < GPB; ++g)
-        sc[t][g] = bf16_to_f32(scale[(blk * kBlockN + r) * GPB + g]);
-    }
-    v4u xa[F][4];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int64_t m = m0 + 16 * f + r;
-      const v4u *xr = reinterpret_cast<const v4u *>(x + m * K + b * kBlockK);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        xa[f][j] = m < M ? xr[4 * j + q] : v4u{0, 0, 0, 0};
-    }
+    for (int i = 0; i < XR; ++i)
+      xs[(4 * i + q) * 16 + ((r ^ (4 * i + q)) & 15)] = k.x[i];
+    wave_order();
 #pragma unroll
     for (int g = 0; g < GPB; ++g) {
+      v4u x[F][J];
       v4f start[F];
 #pragma unroll
       for (int f = 0; f < F; ++f) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          x[f][j] = xs[(16 * f + r) * 16 + ((4 * (g * J + j) + q) ^ r)];
         start[f] = v4f{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4 / GPB; ++j)
-          start[f] = mfma(xa[f][g * (4 / GPB) + j], minus8, start[f]);
+        for (int j = 0; j < J; ++j) start[f] = mfma(x[f][j], minus8, start[f]);
       }
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        v8bf wb[4 / GPB];
+        v4f s[F];
 #pragma unroll
-        for (int j = 0; j < 4 / GPB; ++j)
-          wb[j] = codes8(wv[t][g * (4 / GPB) + j]);
+        for (int f = 0; f < F; ++f) s[f] = start[f];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          v4f s = start[f];
+        for (int j = 0; j < J; ++j) {
+          const v8bf w = codes8(k.w[t][g * J + j]);
 #pragma unroll
-          for (int j = 0; j < 4 / GPB; ++j)
-            s = mfma(xa[f][g * (4 / GPB) + j], wb[j], s);
+          for (int f = 0; f < F; ++f) s[f] = mfma(x[f][j], w, s[f]);
+        }
+        const float sc = Scales<G>::get(k.s[t], g);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[f][t][i] = fmaf(s[i], sc[t][g], acc[f][t][i]);
-        }
+            acc[f][t][i] = fmaf(s[f][i], sc, acc[f][t][i]);
       }
     }
+    wave_order();
+  };
+
+  // Two or three blocks of a wave on their way at a time measured no faster (the
+  // waves beside it are what hides a load) and cost the registers for them.
+  Block blk;
+  load(blk, wave);
+  for (int i = threadIdx.x; i < 16 * T; i += (int)blockDim.x) {
+    const int64_t c = (int64_t)tile0 * kBlockN + i;
+    bias_of[i] = p.bias && c < N ? bf16_to_f32(p.bias[c]) : 0.0f;
+  }
+#pragma unroll
+  for (int i = XR; i < 4 * F; ++i) xs[i * 64 + lane] = v4u{0, 0, 0, 0};
+  for (int b = wave; b < p.kblocks; b += W) {
+    multiply(blk);
+    load(blk, min(b + W, p.kblocks - 1));
   }
 
 #pragma unroll
   for (int f = 0; f < F; ++f)
 #pragma unroll
-    for (int t = 0; t < T; ++t) red[wave][f][t][lane] = acc[f][t];
+    for (int t = 0; t < T; ++t) mine[(f * T + t) * 64 + lane] = acc[f][t];
   __syncthreads();
   // A thread finishes four tokens of one channel.
-  for (int o = threadIdx.x; o < F * T * 64; o += W * 64) {
+  for (int o = threadIdx.x; o < F * T * 64; o += (int)blockDim.x) {
     const int f = o / (64 * T), t = o / 64 % T, l = o & 63;
-    v4f s = red[0][f][t][l];
-#pragma unroll
-    for (int w = 1; w < W; ++w) s += red[w][f][t][l];
-    if (tile0 + t >= tiles) continue;
-    const int64_t n = (int64_t)(tile0 + t) * kBlockN + (l & 15);
-    const float b = bias ? bf16_to_f32(bias[n]) : 0.0f;
+    v4f s = smem[o];
+    for (int w = 1; w < W; ++w) s += smem[w * kWaveLds + o];
+    if (tile0 + t >= p.tiles) continue;
+    const int64_t c = (int64_t)(tile0 + t) * kBlockN + (l & 15);
+    const float b = bias_of[16 * t + (l & 15)];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + 16 * f + 4 * (l >> 4) + i;
-      if (m < M) y[m * N + n] = (uint16_t)pack_bf16x2(s[i] + b, 0.0f);
+      const int m = 16 * f + 4 * (l >> 4) + i;
+      if (m < M) p.y[(m0 + m) * N + c] = (uint16_t)pack_bf16x2(s[i] + b, 0.0f);
     }
   }
 }
 
-template <int F, int T, int W>
-hipError_t launch_linear(const uint16_t *x, const uint8_t *w4,
-                         const uint16_t *scale, const uint16_t *bias,
-                         uint16_t *y, int64_t M, int tiles, int kblocks,
-                         int group, hipStream_t stream) {
-  const dim3 grid((unsigned)((tiles + T - 1) / T),
-                  (unsigned)((M + 16 * F - 1) / (16 * F)));
+template <int F, int XR, int T, int WMAX>
+hipError_t launch_linear(const LinearArgs &p, int group, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.tiles + T - 1) / T),
+                  (unsigned)((p.M + 16 * F - 1) / (16 * F)));
+  const int waves = p.kblocks < WMAX ? p.kblocks : WMAX;
+  const dim3 block(64 * waves);
 #define W8A8_W4_LAUNCH(G)                                                   \
-  hipLaunchKernelGGL((w4_linear_kernel<F, T, W, G>), grid, dim3(W * 64), 0, \
-                     stream, x, w4, scale, bias, y, M, tiles, kblocks)
+  hipLaunchKernelGGL((w4_linear_kernel<F, XR, T, WMAX, G>), grid, block, 0,   \
+                     stream, p)
   if (group == 32)
     W8A8_W4_LAUNCH(32);
   else if (group == 64)
@@ -267,6 +363,16 @@ hipError_t launch_linear(const uint16_t *x, const uint8_t *w4,
     W8A8_W4_LAUNCH(128);
 #undef W8A8_W4_LAUNCH
   return hipGetLastError();
+}
+
+// Up to 16 tokens: XR by the tokens, T so that the groups are about one a CU.
+template <int XR>
+hipError_t launch_few(const LinearArgs &p, int group, hipStream_t stream) {
+  if (p.tiles <= kCUs) return launch_linear<1, XR, 1, 16>(p, group, stream);
+  if (p.tiles <= 2 * kCUs) return launch_linear<1, XR, 2, 16>(p, group, stream);
+  if (p.tiles <= 4 * kCUs) return launch_linear<1, XR, 4, 8>(p, group, stream);
+  if (p.tiles <= 6 * kCUs) return launch_linear<1, XR, 6, 8>(p, group, stream);
+  return launch_linear<1, XR, 7, 8>(p, group, stream);
 }
 
 dim3 pack_grid(int64_t blocks) {
@@ -296,16 +402,29 @@ hipError_t launch_w4_pack(const int8_t *codes, const uint16_t *scales,
   return hipGetLastError();
 }
 
+// Groups of about one a CU read x least often for the CUs they fill.  Measured
+// at one token unless said (us; tiles of 16 channels):
+//    336 tiles, K  5376: T 2, 16 waves 5.1; T 1 5.6, T 4 6.5
+//   1344 tiles, K  5376: (8 tokens) T 6, 8 waves 15.9; T 3 17.4, T 4 19.2
+//   1792 tiles, K  5376: T 7 17.6; T 4 17.9, T 2 18.7
+//    336 tiles, K 21504: (32 and 64 tokens) T 2 31, T 3 44; T 6 38, 58
+// From 17 tokens on a group takes 32: 64 tokens through 336 tiles, K 5376 take
+// 9.7 us, as four times 16 tokens 10.7.
 hipError_t launch_w4_linear(const uint16_t *x, const uint8_t *w4,
                             const uint16_t *scale, const uint16_t *bias,
                             uint16_t *y, int64_t M, int64_t N, int64_t K,
                             int group, hipStream_t stream) {
-  const int tiles = (int)(N / kBlockN), kblocks = (int)(K / kBlockK);
-  if (M <= 16)
-    return launch_linear<1, 1, 8>(x, w4, scale, bias, y, M, tiles, kblocks,
-                                  group, stream);
-  return launch_linear<4, 2, 8>(x, w4, scale, bias, y, M, tiles, kblocks,
-                                group, stream);
+  const LinearArgs p{x, w4, scale, bias, y, M, (int)(N / kBlockN),
+                     (int)(K / kBlockK)};
+  if (M <= 4) return launch_few<1>(p, group, stream);
+  if (M <= 8) return launch_few<2>(p, group, stream);
+  if (M <= 16) return launch_few<4>(p, group, stream);
+  const int64_t all = p.tiles * ((M + 31) / 32);
+  if (all <= kCUs) return launch_linear<2, 8, 1, 8>(p, group, stream);
+  if (all <= 2 * kCUs) return launch_linear<2, 8, 2, 8>(p, group, stream);
+  if (all <= 3 * kCUs) return launch_linear<2, 8, 3, 8>(p, group, stream);
+  if (all <= 6 * kCUs) return launch_linear<2, 8, 6, 8>(p, group, stream);
+  return launch_linear<2, 8, 8, 8>(p, group, stream);
 }
 
 }  // namespace w8a8

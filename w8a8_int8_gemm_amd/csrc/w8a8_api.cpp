@@ -637,7 +637,7 @@ int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
                    uint16_t *y, int64_t M, int64_t N, int64_t K,
                    int64_t group, void *stream) {
   if (!x || !w4 || !w4_scale || !y) return W8A8_ERR_NULL;
-  if (M < 1 || M > 64 * 65535) return W8A8_ERR_SHAPE;
+  if (M < 1 || M > 32 * 65535) return W8A8_ERR_SHAPE;
   int st = validate_w4(N, K, group);
   if (st != W8A8_OK) return st;
   if (!aligned(x, 16) || !aligned(w4, 16) || !aligned(w4_scale, 16) ||
