@@ -156,15 +156,25 @@ def _check(fn: str, status: int):
 # torch-facing wrappers
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream=None):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The handle of `stream`, or of the current GPU's current stream (read
+    without building a stream object: a call's host time is a few such steps,
+    and at a few tokens it is as long as the kernels)."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _on_stream(stream, *tensors):
@@ -183,7 +193,7 @@ def _on_stream(stream, *tensors):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, dtype, ndim, name, shape=None):
@@ -193,15 +203,21 @@ def _need(t, dtype, ndim, name, shape=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or t.dim() != ndim or not t.is_contiguous():
+    size = t.shape
+    if t.dtype != dtype or len(size) != ndim or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} with {ndim} "
-                         f"dims, got {t.dtype} {tuple(t.shape)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+                         f"dims, got {t.dtype} {tuple(size)}")
+    if shape is not None and size != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)}")
+                         f"{tuple(size)}")
+    _on_current_gpu(t, name)
+
+
+def _on_current_gpu(t, name):
+    torch = _torch()
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current GPU "
                          f"(cuda:{torch.cuda.current_device()})")
 
@@ -473,54 +489,57 @@ def quantize_act_swiglu(h, *, out=None, stream=None):
 
 def _norm_arg(kind, weight, bias, eps, H, name):
     """A w8a8_norm_t; the vectors must outlive the call."""
-    torch = _torch()
-    if kind not in NORM_KINDS:
+    code = NORM_KINDS.get(kind)
+    if code is None:
         raise ValueError(f"{name}: expected one of {sorted(NORM_KINDS)}, got "
                          f"{kind!r}")
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _need(t, torch.bfloat16, 1, f"{name} {what}", (H,))
-    return _Norm(NORM_KINDS[kind], eps,
-                 None if weight is None else weight.data_ptr(),
-                 None if bias is None else bias.data_ptr())
+    w = b = None
+    if weight is not None:
+        _need(weight, _torch().bfloat16, 1, f"{name} weight", (H,))
+        w = weight.data_ptr()
+    if bias is not None:
+        _need(bias, _torch().bfloat16, 1, f"{name} bias", (H,))
+        b = bias.data_ptr()
+    return _Norm(code, eps, w, b)
 
 
-def _mod_arg(M, H, mod_row, **vectors):
+def _mod_arg(M, H, mod_row, scale=None, shift=None, gate=None):
     """A w8a8_modulation_t from bf16 vectors [H] or tables [rows, H] (rows at
-    any stride, their values contiguous) that agree on `rows`."""
+    any stride, their values contiguous) that agree on `rows`; None without
+    any."""
     torch = _torch()
-    mod = _Modulation()
-    rows = None
-    for name, t in vectors.items():
+    ptr, step, rows = [None] * 3, [0] * 3, None
+    for i, t in enumerate((scale, shift, gate)):
         if t is None:
             continue
+        name = ("scale", "shift", "gate")[i]
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if (t.dtype != torch.bfloat16 or t.dim() not in (1, 2) or
-                t.shape[-1] != H or (H > 1 and t.stride(-1) != 1)):
+        size = t.shape
+        if (t.dtype != torch.bfloat16 or len(size) not in (1, 2) or
+                size[-1] != H or (H > 1 and t.stride(-1) != 1)):
             raise ValueError(f"{name}: expected {torch.bfloat16} [{H}] or "
                              f"[rows, {H}] with contiguous rows, got "
-                             f"{t.dtype} {tuple(t.shape)}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on the GPU")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must be on the current GPU "
-                             f"(cuda:{torch.cuda.current_device()})")
-        n = 1 if t.dim() == 1 else t.shape[0]
+                             f"{t.dtype} {tuple(size)}")
+        _on_current_gpu(t, name)
+        n = 1 if len(size) == 1 else size[0]
         if rows is not None and n != rows:
             raise ValueError(f"{name}: {n} rows, the other vectors have "
                              f"{rows}")
         rows = n
-        setattr(mod, name, t.data_ptr())
-        setattr(mod, name + "_stride", 0 if n == 1 else t.stride(0))
+        ptr[i] = t.data_ptr()
+        step[i] = 0 if n == 1 else t.stride(0)
+    row = None
     if mod_row is not None:
         _need(mod_row, torch.int32, 1, "mod_row", (M,))
-        mod.row = mod_row.data_ptr()
-    elif rows not in (None, 1, M):
+        row = mod_row.data_ptr()
+        if rows is None:  # the index says only which tokens are padding
+            rows = 2**31 - 1
+    elif rows is None:
+        return None
+    elif rows != 1 and rows != M:
         raise ValueError(f"{rows} modulation rows for {M} tokens need mod_row")
-    # without vectors mod_row says only which tokens are padding
-    mod.rows = rows if rows is not None else 2**31 - 1 if mod.row else 0
-    return mod
+    return _Modulation(*ptr, *step, rows, row)
 
 
 def norm_modulate(x, *, norm="rms", weight=None, bias=None, eps=1e-6,
