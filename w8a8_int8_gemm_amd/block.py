@@ -183,3 +183,145 @@ class BlockRunner:
                   out=(self.hq, self.hs))
         gemm("fc2", self.hq, self.hs)
         return self.out
+
+
+# ---------------------------------------------------------------------------
+# a block with its norms, gates and residuals
+# ---------------------------------------------------------------------------
+
+@dataclass
+class DeviceProj4:
+    """A projection with packed 4-bit weights, for a few tokens."""
+    name: str
+    N: int
+    K: int
+    w4: object        # uint8 [N/16, K/128, 64, 16]
+    w4_scale: object  # bf16 [N/16, K/128, 16, 128/group]
+    bias: object      # bf16 [N]
+
+
+def to_four_bit(p: DeviceProj, group: int = 128) -> DeviceProj4:
+    """The 4-bit form of an INT8 projection (its weights w * sw in BF16
+    through the converter)."""
+    import torch
+    w = (p.w.float() * p.sw[:, None]).to(torch.bfloat16)
+    return DeviceProj4(p.name, p.N, p.K, *B.w4_quantize_weight(w, group=group),
+                       p.bias)
+
+
+@dataclass
+class BlockNorms:
+    """What stands between a block's projections (every vector bf16 [H] or
+    None).  ``table`` bf16 [rows, 6 H] holds the modulation of a row as
+    shift, scale and gate of the attention side, then of the MLP side;
+    ``mod_row`` int32 [M] names each token's row (None: one row for all, or
+    one for each token; a row outside the table marks a padding token)."""
+    table: object
+    mod_row: object = None
+    norm: str = "rms"             # in front of Q, K, V and of FC1
+    weight: tuple = (None, None)
+    bias: tuple = (None, None)
+    post_norm: str = "none"       # behind the attention output and FC2
+    post_weight: tuple = (None, None)
+    post_bias: tuple = (None, None)
+    residual_scale: float = 1.0
+    eps: float = 1e-6
+
+    def before(self, side: int) -> dict:
+        """Keywords of the norm in front of side 0 (attention) or 1 (MLP)."""
+        H = self.table.shape[1] // 6
+        at = 3 * side * H
+        return dict(norm=self.norm, weight=self.weight[side],
+                    bias=self.bias[side], eps=self.eps,
+                    shift=self.table[:, at:at + H],
+                    scale=self.table[:, at + H:at + 2 * H])
+
+    def behind(self, side: int) -> dict:
+        """Keywords of the gate and residual behind that side."""
+        H = self.table.shape[1] // 6
+        at = (3 * side + 2) * H
+        return dict(post_norm=self.post_norm,
+                    post_weight=self.post_weight[side],
+                    post_bias=self.post_bias[side], post_eps=self.eps,
+                    residual_scale=self.residual_scale,
+                    gate=self.table[:, at:at + H])
+
+
+class NormedBlock:
+    """A whole block without its attention: norm and modulation, Q, K, V, the
+    attention output projection (fed by V's output, the attention result's
+    shape), gate and residual, the next norm, the MLP, gate and residual.
+    Buffers are preallocated for one token count.  With ``four_bit`` the
+    projections are DeviceProj4 and activations stay BF16 (a few tokens);
+    otherwise DeviceProj, and the norms write INT8 codes."""
+
+    def __init__(self, M: int, projs=D.BLOCK_PROJS, mlp: str = "silu",
+                 four_bit: bool = False, device="cuda"):
+        import torch
+        self.M, self.mlp, self.four_bit = M, mlp, four_bit
+        shape = {p.name: (p.N, p.K) for p in projs}
+        H = shape["q"][1]
+        bf, i8, f32 = torch.bfloat16, torch.int8, torch.float32
+        e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=device)
+        self.out = {n: e(M, N) for n, (N, _) in shape.items()}
+        self.r = e(M, H)
+        if four_bit:
+            self.y = e(M, H)
+            self.h = e(M, shape["fc2"][1])
+            return
+        self.yq, self.ys = e(M, H, dt=i8), e(M, dt=f32)
+        self.oq, self.os = e(M, shape["o"][1], dt=i8), e(M, dt=f32)
+        self.hq, self.hs = e(M, shape["fc2"][1], dt=i8), e(M, dt=f32)
+        need = max(B.gemm_workspace_bytes(M, N, K) for N, K in shape.values())
+        self.ws = e(max(need, 256), dt=torch.uint8)
+
+    def run(self, x, projs: dict, norms: BlockNorms, out=None, stream=None):
+        """x: bf16 [M, H] -> bf16 [M, H] (``out``, or a new tensor)."""
+        run = self._run4 if self.four_bit else self._run8
+        rows = dict(mod_row=norms.mod_row, stream=stream)
+        return run(x, projs, norms, rows, out, stream)
+
+    def _run8(self, x, projs, norms, rows, out, stream):
+        def gemm(name, q, s):
+            p = projs[name]
+            B.gemm(q, s, p.w, p.sw, p.bias, out=self.out[name],
+                   workspace=self.ws, stream=stream)
+
+        y = (self.yq, self.ys)
+        B.norm_modulate_quantize(x, **norms.before(0), **rows, out=y)
+        for n in ("q", "k", "v"):
+            gemm(n, *y)
+        B.quantize_act(self.out["v"], out=(self.oq, self.os), stream=stream)
+        gemm("o", self.oq, self.os)
+        B.gated_residual_norm_quantize(
+            x, self.out["o"], **norms.behind(0), **norms.before(1), **rows,
+            out=(self.r, *y))
+        gemm("fc1", *y)
+        h = (self.hq, self.hs)
+        if self.mlp == "swiglu":
+            B.quantize_act_swiglu(self.out["fc1"], out=h, stream=stream)
+        else:
+            B.quantize_act(self.out["fc1"], silu=True, out=h, stream=stream)
+        gemm("fc2", *h)
+        return B.gated_residual(self.r, self.out["fc2"], **norms.behind(1),
+                                **rows, out=out)
+
+    def _run4(self, x, projs, norms, rows, out, stream):
+        def linear(name, a):
+            p = projs[name]
+            B.w4_linear(a, p.w4, p.w4_scale, p.bias, out=self.out[name],
+                        stream=stream)
+
+        B.norm_modulate(x, **norms.before(0), **rows, out=self.y)
+        for n in ("q", "k", "v"):
+            linear(n, self.y)
+        linear("o", self.out["v"])
+        B.gated_residual_norm(x, self.out["o"], **norms.behind(0),
+                              **norms.before(1), **rows,
+                              out=(self.r, self.y))
+        linear("fc1", self.y)
+        act = B.swiglu if self.mlp == "swiglu" else B.silu
+        act(self.out["fc1"], out=self.h, stream=stream)
+        linear("fc2", self.h)
+        return B.gated_residual(self.r, self.out["fc2"], **norms.behind(1),
+                                **rows, out=out)
