@@ -300,7 +300,7 @@ int w8a8_quantize_act_silu(const uint16_t *x, int64_t M, int64_t K,
  * quantizing forms take y before any rounding to BF16: the scale is
  * max|y| / 127 and the codes are the integers nearest to y / scale in [-127,
  * 127] (taken as y times the reciprocal: either neighbour where y / scale lies
- * within 2^-15 of a half; a row of zeros has scale 0 and codes 0).
+ * within 2^-16 of a half; a row of zeros has scale 0 and codes 0).
  * (norm_modulate followed by quantize_act quantizes the rounded y instead, and
  * may differ by a code.)
  *

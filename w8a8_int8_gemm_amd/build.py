@@ -25,7 +25,7 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libw8a8.so"
 SOURCES = ["w8a8_api.cpp", "rowwise.hip", "gemm.hip", "norm.hip", "w4.hip"]
 # Headers the library's sources include (part of its build id).
-HEADERS = [CSRC / "internal.h", CSRC / "rowwise.h", CSRC / "quant.h",
+HEADERS = [CSRC / "internal.h", CSRC / "rowwise.h",
            CSRC / "norm.h", CSRC / "w4.h", ROOT / "include" / "w8a8.h"]
 # Measurement support, not part of the library: the register-only MFMA
 # rate on given code matrices (loaded by bench.py only).

@@ -272,9 +272,9 @@ __device__ __forceinline__ Affine pre_map(const NormArgs &a, const PreVecs &p,
 }
 
 // Scale and reciprocal of a row whose largest magnitude is amax.  The codes
-// are the nearest integers to y * (1 / s): those of y / s but where that lies
-// within 2^-15 of a half (y itself is known no better: the reciprocal is off
-// by 2^-23 and the product by 2^-24 of at most 127, the sum by 2^-17).
+// are the integers nearest to y * (1 / s), rounded once: those of y / s but
+// where that lies within 2^-16 of a half, since the reciprocal is off by a
+// little over 2^-24 of at most 127 (y itself is known no better).
 struct CodeRow {
   float s, r;
 };
@@ -287,26 +287,37 @@ constexpr float kSmallScale = 0x1p-100f, kLift = 0x1p64f;
 // overflow; its scale says so (NaN).
 __device__ __forceinline__ CodeRow code_row(float amax, float f) {
   const float s = f > 0.0f ? amax / 127.0f : __builtin_nanf("");
-  const float r = __builtin_amdgcn_rcpf(s < kSmallScale ? s * kLift : s);
+  const float d = s < kSmallScale ? s * kLift : s;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(fmaf(-d, r, 1.0f), r, r);  // Newton's step: to within half a step
   // the same in every lane: keep it in scalar registers
   return CodeRow{
       __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(s))),
       __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(r)))};
 }
 
-// Biased codes of 8 values.  A subnormal scale is so coarse that y / s may pass
-// 127; the conversion clamps above, the maximum below.
+// Codes of 8 values.  At 1.5 * 2^23 a binary32 step is 1, so one fused
+// multiply-add rounds y * r to the nearest integer, ties to even, and leaves
+// its two's complement in the low byte.  A subnormal scale is so coarse that
+// y / s may pass 127 and is clamped.
 template <bool SMALL>
 __device__ __forceinline__ uint2 codes8(const F8 &y, float r) {
-  uint32_t o[2] = {0, 0};
+  uint32_t c[8], o[2];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float u = SMALL ? fmaxf(fmaf(y.v[e] * kLift, r, 128.0f), 1.0f)
-                          : fmaf(y.v[e], r, 128.0f);
-    o[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(u, e % 4, o[e / 4]);
+    const float v =
+        SMALL ? fminf(fmaxf(y.v[e] * kLift * r, -127.0f), 127.0f) : y.v[e];
+    c[e] = __float_as_uint(fmaf(v, SMALL ? 1.0f : r, 0x1.8p23f));
   }
-  // biased bytes -> two's complement codes
-  return make_uint2(o[0] ^ 0x80808080u, o[1] ^ 0x80808080u);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h],
+                                              0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2],
+                                              0x04000C0Cu);
+    o[h] = lo | hi;
+  }
+  return make_uint2(o[0], o[1]);
 }
 
 __device__ __forceinline__ uint2 codes8(const F8 &y, const CodeRow &c) {
