@@ -250,6 +250,8 @@ def test_special_rows():
             assert got[0][7].isnan().all()
     y = call(x, {"norm_kind": "rms"})
     assert y[7].isnan().all() and y[8].isnan().any()
+    one = torch.full((3, 5376), 0.7, dtype=BF, device="cuda")
+    assert (call(one, {"norm_kind": "layer"}) == 0).all()  # exactly
     for kind in ("rms", "layer"):
         s = call(x, {"norm_kind": kind}, True)[1]
         assert s[[7, 8]].isnan().all() and s[fine].isfinite().all()

@@ -125,11 +125,12 @@ struct Reducer {
   }
 };
 
-// A row's statistics as the map v -> v * f + c that normalizes it: f =
-// 1 / sqrt(mean square + eps), c = -mean * f.  The mean first, then the squares
-// of the differences, so that a large mean costs the variance no digits.
+// A row's statistics: it is normalized by (v - mean) * f, f =
+// 1 / sqrt(mean square + eps), the mean 0 but for a layer norm.  The mean first,
+// then the squares of the differences, so that a large mean costs the variance
+// no digits; a constant row is exactly zero.
 struct Stats {
-  float f, c;
+  float f, mean;
 };
 
 // `Row` gives chunk i of row r (CH chunks a thread, thread t of `step`; places
@@ -138,7 +139,7 @@ struct Stats {
 template <int R, int CH, class Row, class Squares, class Again>
 __device__ __forceinline__ void row_stats(Stats (&st)[R], int kind, float eps,
                                           int t, int step, int chunks,
-                                          float inv_h, Reducer<R> &red,
+                                          float width, Reducer<R> &red,
                                           Row row, Squares squares,
                                           Again again) {
   float sq[R], mean[R];
@@ -161,7 +162,7 @@ __device__ __forceinline__ void row_stats(Stats (&st)[R], int kind, float eps,
     again();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      mean[r] *= inv_h;
+      mean[r] /= width;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const F8 v = row(r, i);
@@ -183,8 +184,8 @@ __device__ __forceinline__ void row_stats(Stats (&st)[R], int kind, float eps,
   again();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    st[r].f = rsqrtf(sq[r] * inv_h + eps);
-    st[r].c = -mean[r] * st[r].f;
+    st[r].f = rsqrtf(sq[r] / width + eps);
+    st[r].mean = mean[r];
   }
 }
 
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
   Reducer<R> red{part, 0};
   const int t = threadIdx.x, step = blockDim.x;
   const int chunks = a.H >> 3;
-  const float inv_h = 1.0f / (float)a.H;
+  const float width = (float)a.H;
   const int64_t m0 = (int64_t)blockIdx.x * R;
   // chunk j of row m0 + r
   auto chunk = [&](const void *p, int r, uint32_t j) {
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
       if (same && i * step + t < chunks)
         gv[i] = post_vecs(a, mr[0], i * step + t);
     row_stats<R, CH>(
-        st, a.post_kind, a.post_eps, t, step, chunks, inv_h, red,
+        st, a.post_kind, a.post_eps, t, step, chunks, width, red,
         [&](int r, int i) { return unpack8(b[r][i]); },
         [&](int r, int i, float sq) { return squares8(b[r][i], sq); },
         [&]() { forget(b); });
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
           const F8 xi = unpack8(x[r][i]), bi = unpack8(b[r][i]);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            v[r][i].v[e] = fmaf(fmaf(bi.v[e], st[r].f, st[r].c), g.a.v[e],
+            v[r][i].v[e] = fmaf((bi.v[e] - st[r].mean) * st[r].f, g.a.v[e],
                                 fmaf(a.residual_scale, xi.v[e], g.b.v[e]));
           o = pack8(v[r][i]);
         }
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
   if (OUT == OUT_NONE) return;
   load_pre();
   row_stats<R, CH>(
-      st, a.kind, a.eps, t, step, chunks, inv_h, red,
+      st, a.kind, a.eps, t, step, chunks, width, red,
       [&](int r, int i) { return RES ? v[r][i] : unpack8(x[r][i]); },
       [&](int r, int i, float sq) {
         return RES ? squares8(v[r][i], sq) : squares8(x[r][i], sq);
@@ -453,7 +454,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
         if (!RES) v[r][i] = unpack8(x[r][i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          y.v[e] = fmaf(fmaf(v[r][i].v[e], st[r].f, st[r].c), g.a.v[e],
+          y.v[e] = fmaf((v[r][i].v[e] - st[r].mean) * st[r].f, g.a.v[e],
                         g.b.v[e]);
           if (OUT == OUT_CODES) amax[r] = fmaxf(amax[r], fabsf(y.v[e]));
         }
