@@ -215,9 +215,10 @@ def _need(t, dtype, ndim, name, shape=None):
 
 def _on_current_gpu(t, name):
     torch = _torch()
-    if not t.is_cuda:
+    device = t.get_device()  # -1: not on a GPU
+    if device < 0:
         raise ValueError(f"{name} must be on the GPU")
-    if t.get_device() != torch._C._cuda_getDevice():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current GPU "
                          f"(cuda:{torch.cuda.current_device()})")
 
@@ -503,6 +504,9 @@ def _norm_arg(kind, weight, bias, eps, H, name):
     return _Norm(code, eps, w, b)
 
 
+_MOD_NAMES = ("scale", "shift", "gate")
+
+
 def _mod_arg(M, H, mod_row, scale=None, shift=None, gate=None):
     """A w8a8_modulation_t from bf16 vectors [H] or tables [rows, H] (rows at
     any stride, their values contiguous) that agree on `rows`; None without
@@ -512,23 +516,25 @@ def _mod_arg(M, H, mod_row, scale=None, shift=None, gate=None):
     for i, t in enumerate((scale, shift, gate)):
         if t is None:
             continue
-        name = ("scale", "shift", "gate")[i]
+        name = _MOD_NAMES[i]
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        size = t.shape
-        if (t.dtype != torch.bfloat16 or len(size) not in (1, 2) or
-                size[-1] != H or (H > 1 and t.stride(-1) != 1)):
+        size, strides = t.shape, t.stride()
+        dims = len(size)
+        if (t.dtype != torch.bfloat16 or not 1 <= dims <= 2 or
+                size[-1] != H or (H > 1 and strides[-1] != 1)):
             raise ValueError(f"{name}: expected {torch.bfloat16} [{H}] or "
                              f"[rows, {H}] with contiguous rows, got "
                              f"{t.dtype} {tuple(size)}")
         _on_current_gpu(t, name)
-        n = 1 if len(size) == 1 else size[0]
+        n = 1 if dims == 1 else size[0]
         if rows is not None and n != rows:
             raise ValueError(f"{name}: {n} rows, the other vectors have "
                              f"{rows}")
         rows = n
         ptr[i] = t.data_ptr()
-        step[i] = 0 if n == 1 else t.stride(0)
+        if n != 1:
+            step[i] = strides[0]
     row = None
     if mod_row is not None:
         _need(mod_row, torch.int32, 1, "mod_row", (M,))
@@ -556,7 +562,8 @@ def norm_modulate(x, *, norm="rms", weight=None, bias=None, eps=1e-6,
     pre = _norm_arg(norm, weight, bias, eps, H, "norm")
     mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift)
     y = torch.empty_like(x) if out is None else out
-    _need(y, torch.bfloat16, 2, "out", (M, H))
+    if out is not None:
+        _need(y, torch.bfloat16, 2, "out", (M, H))
     _check("w8a8_norm_modulate", lib().w8a8_norm_modulate(
         _ptr(x), M, H, pre, mod, _ptr(y), _stream(stream)))
     if out is None:
@@ -576,8 +583,8 @@ def norm_modulate_quantize(x, *, norm="rms", weight=None, bias=None,
     pre = _norm_arg(norm, weight, bias, eps, H, "norm")
     mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift)
     if out is None:
-        q = torch.empty((M, H), dtype=torch.int8, device=x.device)
-        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+        q = x.new_empty((M, H), dtype=torch.int8)
+        s = x.new_empty((M,), dtype=torch.float32)
     else:
         q, s = out
         _need(q, torch.int8, 2, "out[0]", (M, H))
@@ -603,7 +610,8 @@ def gated_residual(x, branch, *, gate=None, residual_scale=1.0,
                      "post_norm")
     mod = _mod_arg(M, H, mod_row, gate=gate)
     r = torch.empty_like(x) if out is None else out
-    _need(r, torch.bfloat16, 2, "out", (M, H))
+    if out is not None:
+        _need(r, torch.bfloat16, 2, "out", (M, H))
     _check("w8a8_gated_residual", lib().w8a8_gated_residual(
         _ptr(x), _ptr(branch), M, H, post, mod, residual_scale, _ptr(r),
         _stream(stream)))
@@ -660,8 +668,8 @@ def gated_residual_norm_quantize(x, branch, *, gate=None, residual_scale=1.0,
     mod = _mod_arg(M, H, mod_row, scale=scale, shift=shift, gate=gate)
     if out is None:
         r = torch.empty_like(x)
-        q = torch.empty((M, H), dtype=torch.int8, device=x.device)
-        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+        q = x.new_empty((M, H), dtype=torch.int8)
+        s = x.new_empty((M,), dtype=torch.float32)
     else:
         r, q, s = out
         _need(r, torch.bfloat16, 2, "out[0]", (M, H))
@@ -740,24 +748,25 @@ def w4_linear(x, w4, w4_scale, bias=None, *, out=None, stream=None):
     _need(x, torch.bfloat16, 2, "x")
     M, K = x.shape
     _need(w4, torch.uint8, 4, "w4")
-    if tuple(w4.shape[1:]) != (K // 128, 64, 16) or K % 128:
+    tiles, blocks, lanes, nbytes = w4.shape
+    if lanes != 64 or nbytes != 16 or blocks * 128 != K:
         raise ValueError(f"w4: expected [N/16, {K}/128, 64, 16], got "
                          f"{tuple(w4.shape)}")
-    N = 16 * w4.shape[0]
+    N = 16 * tiles
     _need(w4_scale, torch.bfloat16, 4, "w4_scale")
-    if (tuple(w4_scale.shape[:3]) != (*w4.shape[:2], 16) or
-            w4_scale.shape[3] not in (1, 2, 4)):
-        raise ValueError(f"w4_scale: expected [{w4.shape[0]}, {w4.shape[1]}, "
-                         f"16, 128/group], got {tuple(w4_scale.shape)}")
+    parts = w4_scale.shape[3]
+    if w4_scale.shape != (tiles, blocks, 16, parts) or parts not in (1, 2, 4):
+        raise ValueError(f"w4_scale: expected [{tiles}, {blocks}, 16, "
+                         f"128/group], got {tuple(w4_scale.shape)}")
     if bias is not None:
         _need(bias, torch.bfloat16, 1, "bias", (N,))
     own_out = out is None
     if own_out:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((M, N))
     else:
         _need(out, torch.bfloat16, 2, "out", (M, N))
     _check("w8a8_w4_linear", lib().w8a8_w4_linear(
         _ptr(x), _ptr(w4), _ptr(w4_scale), _ptr(bias), _ptr(out), M, N, K,
-        128 // w4_scale.shape[3], _stream(stream)))
+        128 // parts, _stream(stream)))
     _on_stream(stream, out if own_out else None)
     return out
