@@ -139,9 +139,9 @@ def test_linear_exact(M, G):
         assert torch.equal(y, want.float().to(BF)), (N, K)
 
 
-@pytest.mark.parametrize("M", [1, 4, 5, 8, 9, 16, 17, 33, 64])
-@pytest.mark.parametrize("tiles", [255, 257, 511, 515, 1021, 1027, 1533, 1543,
-                                   1800])
+@pytest.mark.parametrize("M", [1, 4, 5, 8, 9, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("tiles", [128, 130, 255, 257, 384, 386, 511, 515, 767,
+                                   770, 1021, 1027, 1533, 1543, 1800])
 def test_linear_exact_wide(M, tiles):
     """Every number of channel tiles a work group takes, the last group with
     fewer; K of fewer blocks than waves and of one more round."""

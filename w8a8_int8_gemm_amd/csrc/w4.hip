@@ -365,13 +365,16 @@ hipError_t launch_linear(const LinearArgs &p, int group, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Up to 16 tokens: XR by the tokens, T so that the groups are about one a CU.
+// 16 tokens a group, XR by the tokens; T so that the groups (of `all` tiles,
+// counted once for every 16 tokens) are about one a CU.
 template <int XR>
-hipError_t launch_few(const LinearArgs &p, int group, hipStream_t stream) {
-  if (p.tiles <= kCUs) return launch_linear<1, XR, 1, 16>(p, group, stream);
-  if (p.tiles <= 2 * kCUs) return launch_linear<1, XR, 2, 16>(p, group, stream);
-  if (p.tiles <= 4 * kCUs) return launch_linear<1, XR, 4, 8>(p, group, stream);
-  if (p.tiles <= 6 * kCUs) return launch_linear<1, XR, 6, 8>(p, group, stream);
+hipError_t launch_16(const LinearArgs &p, int64_t all, int group,
+                     hipStream_t stream) {
+  if (all <= kCUs) return launch_linear<1, XR, 1, 16>(p, group, stream);
+  if (all <= 2 * kCUs) return launch_linear<1, XR, 2, 16>(p, group, stream);
+  if (all <= 3 * kCUs) return launch_linear<1, XR, 3, 12>(p, group, stream);
+  if (all <= 4 * kCUs) return launch_linear<1, XR, 4, 8>(p, group, stream);
+  if (all <= 6 * kCUs) return launch_linear<1, XR, 6, 8>(p, group, stream);
   return launch_linear<1, XR, 7, 8>(p, group, stream);
 }
 
@@ -407,18 +410,22 @@ hipError_t launch_w4_pack(const int8_t *codes, const uint16_t *scales,
 //    336 tiles, K  5376: T 2, 16 waves 5.1; T 1 5.6, T 4 6.5
 //   1344 tiles, K  5376: (8 tokens) T 6, 8 waves 15.9; T 3 17.4, T 4 19.2
 //   1792 tiles, K  5376: T 7 17.6; T 4 17.9, T 2 18.7
-//    336 tiles, K 21504: (32 and 64 tokens) T 2 31, T 3 44; T 6 38, 58
-// From 17 tokens on a group takes 32: 64 tokens through 336 tiles, K 5376 take
-// 9.7 us, as four times 16 tokens 10.7.
+// From 17 tokens on a group takes 32 of them: 64 tokens through 336 tiles,
+// K 5376, 9.7 us, as four times 16 tokens 10.7; 32 tokens through 1344 tiles
+// 20.0 and 24.9.  But where 16 at a time still make one group a CU of at most
+// three tiles, that is faster: 32 tokens through 336 tiles 7.0 us against 8.3,
+// with K 21504 26.9 against 31.
 hipError_t launch_w4_linear(const uint16_t *x, const uint8_t *w4,
                             const uint16_t *scale, const uint16_t *bias,
                             uint16_t *y, int64_t M, int64_t N, int64_t K,
                             int group, hipStream_t stream) {
   const LinearArgs p{x, w4, scale, bias, y, M, (int)(N / kBlockN),
                      (int)(K / kBlockK)};
-  if (M <= 4) return launch_few<1>(p, group, stream);
-  if (M <= 8) return launch_few<2>(p, group, stream);
-  if (M <= 16) return launch_few<4>(p, group, stream);
+  if (M <= 4) return launch_16<1>(p, p.tiles, group, stream);
+  if (M <= 8) return launch_16<2>(p, p.tiles, group, stream);
+  if (M <= 16) return launch_16<4>(p, p.tiles, group, stream);
+  if (M <= 32 && 2 * p.tiles <= 3 * kCUs)
+    return launch_16<4>(p, 2 * p.tiles, group, stream);
   const int64_t all = p.tiles * ((M + 31) / 32);
   if (all <= kCUs) return launch_linear<2, 8, 1, 8>(p, group, stream);
   if (all <= 2 * kCUs) return launch_linear<2, 8, 2, 8>(p, group, stream);
