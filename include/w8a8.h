@@ -429,8 +429,10 @@ int w8a8_w4_pack_weight(const int8_t *codes, const uint16_t *scales,
 /*
  * The product.  x BF16 [M,K] and y BF16 [M,N], 16-byte aligned; w4 and
  * w4_scale as above; bias BF16 [N], 2-byte aligned, or NULL.  No workspace.
- * Made for a few tokens: beyond 32 the weights are read again for every 32
- * (from there on w8a8_linear is faster where N or K is large).  Shape: 1 <= M <= 32 * 65535; N and K as above.
+ * A token that holds Inf or NaN spoils only its own outputs.  Made for a few
+ * tokens: beyond 32 the weights are read again for every 32 (from there on
+ * w8a8_linear is faster where N or K is large).
+ * Shape: 1 <= M <= 32 * 65535; N and K as above.
  * Errors: NULL, SHAPE, ARG (group), ALIGN, ALIAS (y overlapping an input),
  * DEVICE, HIP.
  */

@@ -126,9 +126,9 @@ struct Reducer {
 };
 
 // A row's statistics: it is normalized by (v - mean) * f, f =
-// 1 / sqrt(mean square + eps), the mean 0 but for a layer norm.  The mean first,
-// then the squares of the differences, so that a large mean costs the variance
-// no digits; a constant row is exactly zero.
+// 1 / sqrt(mean square + eps), the mean 0 but for a layer norm.  The mean
+// first, then the squares of the differences, so that a large mean costs the
+// variance no digits; a constant row is exactly zero.
 struct Stats {
   float f, mean;
 };

@@ -310,8 +310,8 @@ __global__ __launch_bounds__(WMAX * 64) void w4_linear_kernel(LinearArgs p) {
     wave_order();
   };
 
-  // Two or three blocks of a wave on their way at a time measured no faster (the
-  // waves beside it are what hides a load) and cost the registers for them.
+  // Two or three blocks of a wave on their way at a time measured no faster
+  // (the waves beside it are what hides a load) and cost the registers.
   Block blk;
   load(blk, wave);
   for (int i = threadIdx.x; i < 16 * T; i += (int)blockDim.x) {
