@@ -311,8 +311,11 @@ int w8a8_quantize_act_silu(const uint16_t *x, int64_t M, int64_t K,
  * no vector is given.
  *
  * Rows are independent: a row that holds Inf or NaN spoils only itself.
- * Sums of squares must stay below the binary32 range (|x| below about 2^56);
- * behind an RMS or layer norm a row that breaks this has a NaN scale.
+ * Behind an RMS or layer norm the sum of squares must stay below the binary32
+ * range (|v| below about 2^56); where it does not, or v holds Inf or NaN, the
+ * norm's whole row is NaN.  A NaN anywhere in y, from x, the branch or a
+ * vector, makes the row's scale NaN, and an Inf makes it Inf (or NaN); codes
+ * under such a scale mean nothing.  Padding tokens stay as they are said to be.
  */
 typedef enum {
   W8A8_NORM_NONE = 0,

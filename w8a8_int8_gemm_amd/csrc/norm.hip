@@ -49,6 +49,14 @@ __device__ __forceinline__ v4u pack8(const F8 &f) {
              pack_bf16x2(f.v[4], f.v[5]), pack_bf16x2(f.v[6], f.v[7])};
 }
 
+// The larger of m and |v|, NaN if either is (fmaxf would drop it).  Held where
+// it stands: several at once would keep the values before them in registers.
+__device__ __forceinline__ float max_mag(float m, float v) {
+  m = __builtin_elementwise_maximum(m, fabsf(v));
+  asm volatile("" : "+v"(m));
+  return m;
+}
+
 // Chunk j (8 values) of a vector; where there is none, pairs of `absent`.
 constexpr uint32_t kZeros = 0, kOnes = 0x3F803F80u;
 
@@ -58,9 +66,12 @@ __device__ __forceinline__ v4u vec8(const uint16_t *p, uint32_t j,
            : v4u{absent, absent, absent, absent};
 }
 
+// Sum, or the larger of two magnitudes.  Those order as their bits do, with
+// every NaN above Inf: one NaN makes a row's maximum NaN.
 template <bool MAX>
 __device__ __forceinline__ float join(float a, float b) {
-  return MAX ? fmaxf(a, b) : a + b;
+  return MAX ? __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)))
+             : a + b;
 }
 
 template <bool MAX, int CTRL>
@@ -128,7 +139,9 @@ struct Reducer {
 // A row's statistics: it is normalized by (v - mean) * f, f =
 // 1 / sqrt(mean square + eps), the mean 0 but for a layer norm.  The mean
 // first, then the squares of the differences, so that a large mean costs the
-// variance no digits; a constant row is exactly zero.
+// variance no digits.  Where the sum of squares is not finite (Inf or NaN in
+// the row, or squares beyond the range) f is NaN, and with it the whole row: 0
+// would take the row's values out of the result without a trace.
 struct Stats {
   float f, mean;
 };
@@ -184,7 +197,8 @@ __device__ __forceinline__ void row_stats(Stats (&st)[R], int kind, float eps,
   again();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    st[r].f = rsqrtf(sq[r] / width + eps);
+    const float ms = sq[r] / width + eps;
+    st[r].f = ms < __builtin_inff() ? rsqrtf(ms) : __builtin_nanf("");
     st[r].mean = mean[r];
   }
 }
@@ -284,10 +298,9 @@ struct CodeRow {
 // then taken 2^64 times larger.
 constexpr float kSmallScale = 0x1p-100f, kLift = 0x1p64f;
 
-// A row whose factor f is not above zero held Inf, NaN or values whose squares
-// overflow; its scale says so (NaN).
-__device__ __forceinline__ CodeRow code_row(float amax, float f) {
-  const float s = f > 0.0f ? amax / 127.0f : __builtin_nanf("");
+// A NaN in the row is in amax, and so in its scale; the codes mean nothing then.
+__device__ __forceinline__ CodeRow code_row(float amax) {
+  const float s = amax / 127.0f;
   const float d = s < kSmallScale ? s * kLift : s;
   float r = __builtin_amdgcn_rcpf(d);
   r = fmaf(fmaf(-d, r, 1.0f), r, r);  // Newton's step: to within half a step
@@ -456,7 +469,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
         for (int e = 0; e < 8; ++e) {
           y.v[e] = fmaf((v[r][i].v[e] - st[r].mean) * st[r].f, g.a.v[e],
                         g.b.v[e]);
-          if (OUT == OUT_CODES) amax[r] = fmaxf(amax[r], fabsf(y.v[e]));
+          if (OUT == OUT_CODES) amax[r] = max_mag(amax[r], y.v[e]);
         }
       }
       if (OUT == OUT_CODES) v[r][i] = y;
@@ -469,7 +482,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (!in_range(r)) continue;
-    const CodeRow Q = code_row(amax[r], live[r] ? st[r].f : 1.0f);
+    const CodeRow Q = code_row(amax[r]);
     if (t == 0) a.qs[m0 + r] = Q.s;
     uint2 *q = reinterpret_cast<uint2 *>(a.q) + (m0 + r) * (int64_t)chunks;
 #pragma unroll
