@@ -410,7 +410,9 @@ int w8a8_gated_residual_norm_quantize(
  * Converts a BF16 weight [N,K] in a Linear's layout: per group, scale =
  * bf16(max|w| / 7) (1 for a group of zeros, at least the smallest BF16 above
  * zero otherwise) and code = clamp(round_half_even(w / scale), -7, 7), the
- * divisions in binary32.
+ * divisions in binary32.  A group that holds NaN has a NaN scale, one that holds
+ * Inf an infinite one (their codes mean nothing): w8a8_w4_linear gives NaN or
+ * Inf for such a channel.
  *   w 16-byte aligned; w4 and w4_scale 16-byte aligned, overlapping nothing.
  * Shape: 16 <= N < 2^26, N % 16 == 0; 128 <= K <= W8A8_MAX_K, K % 128 == 0;
  * N * K < 2^37 (a launch holds fewer than 2^32 work-items).  Errors: NULL,

@@ -64,6 +64,12 @@ __global__ __launch_bounds__(kPackThreads) void w4_pack_kernel(
         scales[n * (K / group) + k0 / group + q];
 }
 
+// The larger value, NaN if either is: fmaxf would drop the NaN, and its weight
+// would become a code under an ordinary scale.
+__device__ __forceinline__ float larger(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+
 __global__ __launch_bounds__(kPackThreads) void w4_quantize_kernel(
     const uint16_t *w, int64_t blocks, int kblocks, int group, uint8_t *w4,
     uint16_t *scale) {
@@ -86,17 +92,17 @@ __global__ __launch_bounds__(kPackThreads) void w4_quantize_kernel(
     const uint32_t p[4] = {c[d].x, c[d].y, c[d].z, c[d].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      a = fmaxf(a, fmaxf(fabsf(bf16_to_f32(p[e] & 0xFFFFu)),
-                         fabsf(bf16_to_f32(p[e] >> 16))));
-    a = fmaxf(a, __shfl_xor(a, 16, 64));
-    amax[d] = fmaxf(a, __shfl_xor(a, 32, 64));
+      a = larger(a, larger(fabsf(bf16_to_f32(p[e] & 0xFFFFu)),
+                           fabsf(bf16_to_f32(p[e] >> 16))));
+    a = larger(a, __shfl_xor(a, 16, 64));
+    amax[d] = larger(a, __shfl_xor(a, 32, 64));
   }
   if (group >= 64) {
-    amax[0] = amax[1] = fmaxf(amax[0], amax[1]);
-    amax[2] = amax[3] = fmaxf(amax[2], amax[3]);
+    amax[0] = amax[1] = larger(amax[0], amax[1]);
+    amax[2] = amax[3] = larger(amax[2], amax[3]);
   }
   if (group == 128)
-    amax[0] = amax[1] = amax[2] = amax[3] = fmaxf(amax[0], amax[2]);
+    amax[0] = amax[1] = amax[2] = amax[3] = larger(amax[0], amax[2]);
   uint32_t out[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
