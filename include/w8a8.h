@@ -306,9 +306,9 @@ int w8a8_quantize_act_silu(const uint16_t *x, int64_t M, int64_t K,
  *
  * i is the token's modulation row: row[m] when `row` is given, else m when
  * rows == M, else 0 (rows must then be 1).  A row[m] outside [0, rows) marks
- * token m as padding: its branch row is not read, r is x unchanged bit for
- * bit, y and its codes and scale are zero.  `row` needs rows >= 1 also where
- * no vector is given.
+ * token m as padding: what its branch row holds does not count, r is x
+ * unchanged bit for bit, y and its codes and scale are zero.  `row` needs
+ * rows >= 1 also where no vector is given.
  *
  * Rows are independent: a row that holds Inf or NaN spoils only itself.
  * Behind an RMS or layer norm the sum of squares must stay below the binary32

@@ -43,8 +43,8 @@ typedef float f2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
 
 // Two binary32 values -> two BF16 (round to nearest, ties to even) packed in
-// one dword, low half first: gfx950's v_cvt_pk_bf16_f32.  Callers pass
-// finite values or +-Inf, never NaN.
+// one dword, low half first: gfx950's v_cvt_pk_bf16_f32.  Infinities stay as
+// they are and NaN stays NaN.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const bf2v b = __builtin_convertvector(f2v{lo, hi}, bf2v);
   return __builtin_bit_cast(uint32_t, b);

@@ -389,8 +389,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs a) {
   };
   auto in_range = [&](int r) { return R == 1 || m0 + r < a.M; };
 
-  // The vectors of the maps are on their way while a reduction goes on (read
-  // behind it: norm to codes of 37503 x 5376 150 us, so 128).
+  // The vectors of the maps are asked for ahead of a reduction, not behind it
+  // (norm to codes of 37503 x 5376: behind it 150 us, so 128).  Each stands
+  // under a test of its pointer, so that the reduction's wait for the row is a
+  // wait for them as well.
   F8 v[R][CH];  // the residual rows, or the output on its way to codes
   Stats st[R];
   PreVecs pv[CH];

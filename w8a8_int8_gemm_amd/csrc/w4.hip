@@ -323,8 +323,10 @@ __global__ __launch_bounds__(WMAX * 64) void w4_linear_kernel(LinearArgs p) {
     wave_order();
   };
 
-  // Two or three blocks of a wave on their way at a time measured no faster
-  // (the waves beside it are what hides a load) and cost the registers.
+  // A block's loads are issued once the block before is done, x last, and x is
+  // stored to LDS first, so that a wave waits for all of them before a product
+  // and only the waves beside it hide a load.  Two or three blocks on their way
+  // at a time measured no faster in this order and cost the registers.
   Block blk;
   load(blk, wave);
   for (int i = threadIdx.x; i < 16 * T; i += (int)blockDim.x) {
@@ -420,8 +422,10 @@ hipError_t launch_w4_pack(const int8_t *codes, const uint16_t *scales,
   return hipGetLastError();
 }
 
-// Groups of about one a CU read x least often for the CUs they fill.  Measured
-// at one token unless said (us; tiles of 16 channels):
+// Groups of about one a CU read x least often for the CUs they fill; the widest
+// outputs take as many rounds as they need.  Measured at one token unless said
+// (us; tiles of 16 channels), widths between not at all; T goes from 3 to 6 in
+// one step for 32 tokens, where half the CUs hold a group.
 //    336 tiles, K  5376: T 2, 16 waves 5.1; T 1 5.6, T 4 6.5
 //   1344 tiles, K  5376: (8 tokens) T 6, 8 waves 15.9; T 3 17.4, T 4 19.2
 //   1792 tiles, K  5376: T 7 17.6; T 4 17.9, T 2 18.7
