@@ -434,11 +434,12 @@ int w8a8_w4_pack_weight(const int8_t *codes, const uint16_t *scales,
 /*
  * The product.  x BF16 [M,K] and y BF16 [M,N], 16-byte aligned; w4 and
  * w4_scale as above; bias BF16 [N], 2-byte aligned, or NULL.  No workspace.
- * A token that holds Inf or NaN spoils only its own outputs.  Finite inputs
- * overflow nothing on the way to a finite y while their magnitudes in a group
- * sum to less than the binary32 range.  The codes' offset is taken off by
- * groups (the sum of 8 x from that of u x), so that each input costs a few
- * binary32 roundings of |x| (|u - 8| + 16) s, also where its weight is zero.
+ * A token that holds Inf or NaN spoils only its own outputs.  Nothing overflows
+ * on the way to a finite y while the magnitudes of x in a group sum to less than
+ * the binary32 range and the sums over groups stay below 16 times that range.
+ * The codes' offset is taken off by groups (the sum of 8 x from that of u x), so
+ * that each input costs a few binary32 roundings of |x| (|u - 8| + 16) s, also
+ * where its weight is zero.
  * Made for a few tokens: beyond 32 the weights are read again for every 32
  * (from there on w8a8_linear is faster where N or K is large).
  * Shape: 1 <= M <= 32 * 65535; N and K as above.
