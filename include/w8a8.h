@@ -451,6 +451,152 @@ int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
                    uint16_t *y, int64_t M, int64_t N, int64_t K,
                    int64_t group, void *stream);
 
+/*
+ * Heads: what stands between a block's Q, K and V and its output projection.
+ * A row holds the heads of one token behind each other, D values each; rows lie
+ * at any stride (in elements), so that the parts of a fused Q, K, V output can
+ * be passed as they are.
+ */
+
+/*
+ * Rotary table: cosines and sines of a token's positions.
+ *   positions  INT32 or FP32 [T, axes], 4-byte aligned (frame, row and column
+ *              of a token, or its place alone).
+ *   table      FP32 [T, 2, P] out, 16-byte aligned: the P cosines of a token,
+ *              then its P sines; P is the sum of pairs[0 .. axes - 1].
+ * Pair i of axis a turns by position * f(a, i), with p = pairs[a]:
+ *   NONE    f = theta^(-i / p)
+ *   LINEAR  f = theta^(-i / p) / factor
+ *   NTK     f = (theta * factor^(p / (p - 1)))^(-i / p)   (p = 1: f = 1)
+ *   YARN    f = theta^(-i / p) * (ramp / factor + 1 - ramp), ramp = clamp((i -
+ *           low) / (high - low), 0, 1), low = max(floor(at(beta_fast)), 0),
+ *           high = min(ceil(at(beta_slow)), 2 p - 1), at(b) = p *
+ *           ln(original / (2 pi b)) / ln(theta); a high - low below 0.001
+ *           counts as 0.001 ("YaRN", Peng et al., 2023)
+ * and the table holds amplitude * cos and amplitude * sin.  Angles and
+ * frequencies are taken in 64 bits (|angle| 2^-52 off), the result is rounded
+ * to binary32 (6 * 2^-24 of the amplitude off at most).  A position that is NaN or
+ * Inf gives NaN.
+ * Shape: 1 <= T <= 2^24 - 1; 1 <= axes <= 4, each with 1 or more pairs, 256 in
+ * all.  theta finite and > 1, factor finite and >= 1, amplitude finite; for
+ * YARN original finite and > 0, beta_fast and beta_slow finite and > 0.
+ * Errors: NULL, SHAPE, ARG, ALIGN, ALIAS, DEVICE, HIP.
+ */
+#define W8A8_ROPE_MAX_AXES 4
+#define W8A8_ROPE_MAX_PAIRS 256
+
+typedef enum {
+  W8A8_ROPE_NONE = 0,
+  W8A8_ROPE_LINEAR = 1,
+  W8A8_ROPE_NTK = 2,
+  W8A8_ROPE_YARN = 3
+} w8a8_rope_scaling_t;
+
+typedef enum {
+  W8A8_POSITIONS_I32 = 0,
+  W8A8_POSITIONS_F32 = 1
+} w8a8_positions_t;
+
+typedef struct {
+  int axes;
+  int pairs[W8A8_ROPE_MAX_AXES];
+  int scaling;            /* w8a8_rope_scaling_t                            */
+  double theta, factor;   /* factor is not read for NONE                    */
+  double original, beta_fast, beta_slow; /* read for YARN only              */
+  double amplitude;
+} w8a8_rope_t;
+
+int w8a8_rope_table(const void *positions, int position_type, int64_t T,
+                    const w8a8_rope_t *rope, float *table, void *stream);
+
+/*
+ * Norms of queries and keys for each head, with the rotation in the same pass.
+ * Every head of a token is normalized over its D values (the norm of
+ * w8a8_norm_t, with NONE for the rotation alone), then its first 2 P values are
+ * turned by the token's row of a rotary table: pair i's values (a, b) become
+ *   (a cos_i - b sin_i, b cos_i + a sin_i)
+ * all in binary32, rounded to BF16 once.  The pair is (2 i, 2 i + 1) where
+ * `interleaved`, else (i, i + P); values from 2 P on are not turned.
+ *
+ *   q, k     one side each; k may be NULL.
+ *   table    FP32 [rows, 2, P] as above, 16-byte aligned, or NULL (no
+ *            rotation; pairs, rows and row are then not read).
+ *   row      INT32 [M], 4-byte aligned: each token's row of the table; NULL:
+ *            row m (rows == M), or row 0 for all (rows == 1).  A row outside
+ *            [0, rows) marks a padding token: its outputs are zero, whatever
+ *            it holds.
+ * A head that holds Inf or NaN spoils only itself (behind RMS or LAYER all of
+ * it is NaN; without a norm only the pair that holds it).
+ * y may be x itself with the same stride (in place); else no output overlaps
+ * anything (parts of one row that interleave at one stride do not).
+ * Shape: 1 <= M <= 2^24 - 1; 8 <= D <= 256, D % 8 == 0; 1 <= heads <= 4096;
+ * strides multiples of 8, heads * D or more and below 2^30; P % 4 == 0,
+ * 2 P <= D; 1 <= rows < 2^31; M * heads * D < 2^36 for each side, and a launch
+ * of fewer than 2^32 work-items.
+ * Errors: NULL, SHAPE, ARG (norm), ALIGN (x, y, weight, bias, table: 16 bytes),
+ * ALIAS, DEVICE, HIP.
+ */
+typedef struct {
+  const uint16_t *x;  /* BF16 [M] rows of heads * D                         */
+  uint16_t *y;        /* BF16 out, likewise                                  */
+  int64_t heads, x_stride, y_stride;
+  w8a8_norm_t norm;   /* weight and bias BF16 [D], or [heads, D] where        */
+  int per_head;       /* this is not 0                                       */
+} w8a8_heads_t;
+
+int w8a8_head_norm_rope(const w8a8_heads_t *q, const w8a8_heads_t *k,
+                        int64_t M, int64_t D, const float *table,
+                        int64_t pairs, int64_t rows, const int32_t *row,
+                        int interleaved, void *stream);
+
+/*
+ * Attention of queries to keys and values of another length (an encoder's
+ * states, or the block's own tokens), for B sequences at once:
+ *   out = softmax(scale * q k^T) v
+ * for each sequence and head, over all of the sequence's keys.  Query head h
+ * reads key head h / (q_heads / k_heads).
+ *   q, out  BF16, Tq rows of q_heads * D;  k, v  BF16, Tk rows of k_heads * D.
+ *   q_offsets, k_offsets  INT32 [B + 1], 4-byte aligned: sequence b's rows are
+ *           those from offsets[b] to offsets[b + 1] - 1; NULL: B sequences of
+ *           T / B rows each (T % B == 0).
+ *   k_lens  INT32 [B], 4-byte aligned, or NULL: only the first k_lens[b] of a
+ *           sequence's keys count (padding behind; none if not positive).
+ * Offsets do not decrease (where they do, or leave [0, T], rows of out may be
+ * written with any values, but nothing outside of q, k, v and out is touched).
+ * Query rows outside of all sequences are left as they were.  What k and v hold
+ * at keys that do not count does not matter.  A sequence without keys gives
+ * zeros.  Scores, maxima, sums and outputs are held in binary32; weights are
+ * rounded to BF16 for the product with v, and their sum is taken of the rounded
+ * ones.  Inf or NaN in q spoils its own row and head; in k or v that counts,
+ * the rows of its sequence and heads; a row all of whose scores are -Inf is
+ * NaN.
+ * Workspace: w8a8_attention_workspace_bytes of the same sizes, 16-byte aligned,
+ * of this call alone until it is done (it holds the parts of a call whose keys
+ * are split; 0 where they are not).  Every row of a part that is read is
+ * written before, by the same call.
+ * out overlaps nothing (parts of one row that interleave at one stride do not).
+ * Results do not depend on other calls, nor on how work groups run.
+ * Shape: 1 <= B <= 2^20; 1 <= Tq, Tk (0 <= Tk: k and v may then be NULL) and
+ * T * heads < 2^31; 8 <= D <= 128, D % 8 == 0; q_heads a multiple of k_heads;
+ * strides multiples of 8, heads * D or more and below 2^22; a launch of fewer
+ * than 2^32 work-items.  0 < scale < Inf.
+ * Errors: NULL, SHAPE, ARG (scale), ALIGN (q, k, v, out: 16 bytes), WORKSPACE,
+ * ALIAS, DEVICE, HIP.
+ */
+typedef struct {
+  const uint16_t *q, *k, *v;
+  uint16_t *out;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int64_t Tq, Tk, B;
+  int64_t q_heads, k_heads, D;
+  const int32_t *q_offsets, *k_offsets, *k_lens;
+  float scale;
+} w8a8_attention_t;
+
+size_t w8a8_attention_workspace_bytes(const w8a8_attention_t *a);
+int w8a8_attention(const w8a8_attention_t *a, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

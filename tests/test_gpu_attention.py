@@ -1,0 +1,348 @@
+"""Attention on the GPU against its definition in 64 bits."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+from tests import headref as R
+from w8a8_int8_gemm_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+BF = torch.bfloat16
+NAN, INF = float("nan"), float("inf")
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def rand(g, *shape, std=1.0, mean=0.0):
+    return (mean + std * torch.randn(*shape, generator=g, device="cuda")).to(BF)
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def starts(n):
+    out = [0]
+    for x in n:
+        out.append(out[-1] + x)
+    return out
+
+
+def inputs(Tq, Tk, Hq, Hk, D, seed, std=1.5):
+    g = gen(seed)
+    return (rand(g, Tq, Hq, D, std=std), rand(g, Tk, Hk, D, std=std),
+            rand(g, Tk, Hk, D, mean=0.2))
+
+
+def check(q, k, v, B_=1, rows=None, **kw):
+    """The call against 64 bits; rows of no sequence stay as they were."""
+    offs = {n: kw.get(n) for n in ("q_offsets", "k_offsets", "k_lens")}
+    spans = R.sequences(q.shape[0], k.shape[0], B_, **offs)
+    out = kw.pop("out", None)
+    if out is None:
+        out = torch.full(q.shape, 77.0, dtype=BF, device="cuda")
+    got = B.attention(q, k, v, out=out, **kw)
+    assert got is out
+    want, bound, covered = R.attention(q, k, v, spans, kw.get("scale"))
+    R.check_bf16(got[covered], want[covered], bound[covered])
+    assert (got[~covered] == 77.0).all()
+    return got
+
+
+WIDTHS = [8, 32, 40, 64, 72, 80, 96, 104, 128]
+LENGTHS = [(1, 1), (1, 63), (3, 64), (32, 65), (33, 127), (64, 300), (65, 1),
+           (200, 129), (257, 191), (512, 64), (300, 600)]
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("Lq,Lk", LENGTHS)
+def test_one_sequence(Lq, Lk, D):
+    check(*inputs(Lq, Lk, 2, 2, D, Lq + Lk + D))
+
+
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (6, 2), (8, 1), (56, 56), (40, 8),
+                                   (9, 3)])
+@pytest.mark.parametrize("Lq,Lk", [(1, 200), (5, 77), (130, 260)])
+def test_shared_heads(Lq, Lk, Hq, Hk):
+    check(*inputs(Lq, Lk, Hq, Hk, 64, Hq + Lq))
+
+
+@pytest.mark.parametrize("Lq,Lk,Hq,Hk,D", [
+    (1, 4096, 2, 2, 128), (1, 5000, 8, 1, 128), (64, 9001, 3, 3, 64),
+    (20, 3000, 4, 2, 40), (1, 100000, 1, 1, 32), (300, 2500, 1, 1, 128),
+    (65, 2049, 2, 1, 96)])
+def test_split_keys(Lq, Lk, Hq, Hk, D):
+    q, k, v = inputs(Lq, Lk, Hq, Hk, D, Lk)
+    assert B.attention_workspace_bytes(Lq, Lk, Hq, Hk, D) > 0
+    check(q, k, v)
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("q_len,k_len", [
+    ([1, 1, 1], [5, 0, 300]), ([0, 7, 0, 40], [3, 0, 64, 65]),
+    ([300, 1, 0, 129], [1, 1000, 7, 0]), ([2] * 70, [i for i in range(70)]),
+    ([1] * 5, [4000, 1, 0, 129, 2000])])
+@pytest.mark.parametrize("Hq,Hk", [(2, 2), (6, 2)])
+def test_packed(q_len, k_len, Hq, Hk, D):
+    q, k, v = inputs(sum(q_len) + 3, sum(k_len) + 2, Hq, Hk, D, 3)
+    n = len(q_len)
+    kw = dict(q_offsets=ints(starts(q_len)), k_offsets=ints(starts(k_len)))
+    # what no sequence holds does not matter
+    k[sum(k_len):], v[sum(k_len):] = NAN, INF
+    got = check(q, k, v, n, **kw)
+    for b, (q0, nq, _, nk) in enumerate(R.sequences(
+            q.shape[0], k.shape[0], n, **kw)):
+        if nk == 0:
+            assert (got[q0:q0 + nq] == 0).all()
+    # sequences that begin behind the first row, some keys left out
+    shift = dict(q_offsets=ints([x + 2 for x in starts(q_len)]),
+                 k_offsets=ints(starts(k_len)),
+                 k_lens=ints([x // 2 for x in k_len]))
+    check(q, k, v, n, **shift)
+
+
+@pytest.mark.parametrize("Lq,Lk", [(1, 512), (70, 100), (300, 333)])
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 4, 128), (6, 2, 64)])
+def test_padded_batch(Lq, Lk, Hq, Hk, D):
+    lens = [Lk, 0, 1, Lk // 2, -5, Lk + 100, 64, 65]
+    n = len(lens)
+    g = gen(Lq)
+    q = rand(g, n, Lq, Hq, D, std=1.5)
+    k, v = rand(g, n, Lk, Hk, D, std=1.5), rand(g, n, Lk, Hk, D)
+    junk = [NAN, INF, -INF, torch.finfo(BF).min]
+    for b, m in enumerate(lens):
+        m = min(max(m, 0), Lk)
+        k[b, m:] = junk[b % 4]
+        v[b, m:] = junk[(b + 1) % 4]
+    got = B.attention(q, k, v, k_lens=ints(lens))
+    assert got.shape == q.shape
+    flat = [t.flatten(0, 1) for t in (q, k, v)]
+    spans = R.sequences(n * Lq, n * Lk, n, k_lens=ints(lens))
+    want, bound, _ = R.attention(*flat, spans)
+    R.check_bf16(got.flatten(0, 1), want, bound)
+    assert (got[[1, 4]] == 0).all()
+    # queries packed, keys a batch
+    kw = dict(q_offsets=ints([b * Lq for b in range(n + 1)]), k_lens=ints(lens))
+    assert torch.equal(B.attention(*flat, **kw), check(*flat, n, **kw))
+    # a batch of one
+    one = B.attention(q[:1], k[:1], v[:1])
+    spans = R.sequences(Lq, Lk, 1)
+    want, bound, _ = R.attention(q[0], k[0], v[0], spans)
+    R.check_bf16(one[0], want, bound)
+
+
+def test_parts_of_a_fused_output():
+    """q, k, v at the stride of a fused Q, K, V; out within wider rows."""
+    M, H, D = 150, 4, 64
+    qkv = rand(gen(1), M, 3 * H * D)
+    q, k, v = (qkv[:, i * H * D:(i + 1) * H * D].unflatten(1, (H, D))
+               for i in range(3))
+    wide = torch.full((M, H * D + 16), 5.0, dtype=BF, device="cuda")
+    out = wide[:, 8:8 + H * D].unflatten(1, (H, D))
+    check(q, k, v, out=out)
+    assert (wide[:, :8] == 5).all() and (wide[:, 8 + H * D:] == 5).all()
+    dense = B.attention(*(t.contiguous() for t in (q, k, v)))
+    assert torch.equal(out, dense)
+    # the result beside the inputs, in the place of another part of their rows
+    both = torch.cat([qkv, torch.zeros_like(qkv[:, :H * D])], 1)
+    a = [both[:, i * H * D:(i + 1) * H * D].unflatten(1, (H, D))
+         for i in range(4)]
+    B.attention(*a[:3], out=a[3])
+    assert torch.equal(a[3], dense) and torch.equal(both[:, :3 * H * D], qkv)
+
+
+@pytest.mark.parametrize("Lq,Lk", [(1, 700), (40, 700), (300, 700)])
+@pytest.mark.parametrize("how", ["rising", "falling", "one", "equal", "scaled",
+                                 "large"])
+def test_running_maximum(Lq, Lk, how):
+    """Scores that move the maximum at every step, or never."""
+    H, D = 2, 64
+    q, k, v = inputs(Lq, Lk, H, H, D, 5)
+    kw = {}
+    if how in ("rising", "falling"):
+        ramp = torch.linspace(-40, 40, Lk, device="cuda")
+        if how == "falling":
+            ramp = -ramp
+        q[:], k[:] = 0, 0
+        q[..., 0] = 4.0
+        k[..., 0] = ramp[:, None].to(BF)
+    elif how == "one":
+        k[Lk // 3] = 8 * q[0].sign()
+    elif how == "equal":
+        q[:] = 0
+    elif how == "scaled":
+        kw["scale"] = 0.01
+    else:
+        q, k = 30 * q, 30 * k  # scores of tens of thousands
+    check(q, k, v, **kw)
+
+
+@pytest.mark.parametrize("Lq", [1, 40, 300])
+def test_nonfinite_values(Lq):
+    q, k, v = inputs(Lq, 200, 4, 2, 64, 6)
+    clean = B.attention(q, k, v)
+    q[0, 1, 5] = NAN
+    got = B.attention(q, k, v)
+    assert got[0, 1].isnan().all()
+    got[0, 1] = clean[0, 1]
+    assert torch.equal(got, clean)
+    q, k, v = inputs(Lq, 200, 4, 2, 64, 6)
+    for bad in (NAN, INF):
+        k2, v2 = k.clone(), v.clone()
+        k2[150, 0, 3] = NAN
+        v2[199, 1, 7] = bad
+        got = B.attention(q, k2, v2)
+        assert got[:, :2].isnan().all()       # heads of key head 0
+        assert not got[:, 2:, 7].isfinite().any()
+        got[:, 2:, 7] = clean[:, 2:, 7]
+        want, bound, _ = R.attention(q, k, v, R.sequences(Lq, 200, 1))
+        R.check_bf16(got[:, 2:], want[:, 2:], bound[:, 2:])
+    # every score -Inf
+    q[:] = 1.0
+    k[:] = -INF
+    assert B.attention(q, k, v).isnan().all()
+    # one finite score among -Inf takes everything
+    k[17] = 0.0
+    assert torch.equal(B.attention(q, k, v),
+                       v[17].repeat_interleave(2, 0).expand(Lq, 4, 64))
+
+
+@pytest.mark.parametrize("Tk", [5, 4000])
+def test_offsets_that_lie_outside_touch_nothing_else(Tk):
+    """Offsets past the ends, and decreasing ones: only q, k, v and out are
+    touched (here between rows of canaries)."""
+    Tq, H, D = 50, 2, 64
+    q, k, v = inputs(Tq, Tk, H, H, D, 7)
+    wide = torch.full((Tq + 200, H, D), 3.0, dtype=BF, device="cuda")
+    out = wide[100:100 + Tq]
+    for qo, ko in (([-5, 20, 90], [-7, 3, Tk + 1000]),
+                   ([30, 10, 40], [Tk, 0, 4]),
+                   ([2**31 - 1, -2**31, 2**31 - 1], [2**31 - 1, 0, -2**31])):
+        B.attention(q, k, v, q_offsets=ints(qo), k_offsets=ints(ko), out=out)
+        torch.cuda.synchronize()
+        assert (wide[:100] == 3).all() and (wide[100 + Tq:] == 3).all()
+    # ends past the rows are taken as the rows' end
+    got = B.attention(q, k, v, q_offsets=ints([0, 20, 90]),
+                      k_offsets=ints([0, 3, Tk + 1000]))
+    assert torch.equal(got, B.attention(
+        q, k, v, q_offsets=ints([0, 20, Tq]), k_offsets=ints([0, 3, Tk])))
+
+
+def test_no_keys_at_all():
+    q, k, v = inputs(9, 0, 2, 2, 64, 8)
+    assert (B.attention(q, k, v) == 0).all()
+
+
+@pytest.mark.parametrize("Lq", [1, 300])
+def test_far_keys_of_a_long_cache(Lq):
+    """Keys past 2^32 bytes, in one sequence and as the last of several."""
+    Tk, stride, D = 70000, 1 << 15, 64
+    k = torch.empty(Tk * stride, dtype=BF, device="cuda").as_strided(
+        (Tk, 1, D), (stride, D, 1))
+    v = torch.empty(Tk * stride, dtype=BF, device="cuda").as_strided(
+        (Tk, 1, D), (stride, D, 1))
+    q, kd, vd = inputs(Lq, Tk, 1, 1, D, 9)
+    k.copy_(kd)
+    v.copy_(vd)
+    assert torch.equal(B.attention(q, k, v), check(q, kd, vd))
+    kw = dict(q_offsets=ints([0, 0, Lq]), k_offsets=ints([0, Tk - 333, Tk]))
+    assert torch.equal(B.attention(q, k, v, **kw), check(q, kd, vd, 2, **kw))
+
+
+def test_repeats_bit_for_bit_on_any_stream():
+    for Lq, Lk in ((1, 6000), (600, 300)):
+        q, k, v = inputs(Lq, Lk, 4, 2, 128, 10)
+        want = B.attention(q, k, v)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        got = [B.attention(q, k, v, stream=s) for _ in range(4)]
+        here = [B.attention(q, k, v) for _ in range(4)]
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(t, want) for t in got + here)
+
+
+@pytest.mark.parametrize("Lq,Lk", [(1, 5000), (300, 200)])
+def test_in_a_graph(Lq, Lk):
+    """Two captured graphs with workspaces of their own, replayed with new
+    inputs and eager calls in between."""
+    H, D = 3, 64
+    sets = [inputs(Lq, Lk, H, H, D, 11 + i) for i in range(2)]
+    lens = ints([Lk])
+    outs = [torch.empty_like(s[0]) for s in sets]
+    need = max(B.attention_workspace_bytes(Lq, Lk, H, H, D), 16)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in sets]
+    B.attention(*sets[0], k_lens=lens)
+    torch.cuda.synchronize()
+    graphs = []
+    for s, o, w in zip(sets, outs, ws):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.attention(*s, k_lens=lens, out=o, workspace=w)
+        graphs.append(g)
+    for i in range(3):
+        for s in sets:
+            for t, n in zip(s, inputs(Lq, Lk, H, H, D, 50 + i)):
+                t.copy_(n)
+        lens.fill_(Lk - 70 * i)
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for s, o in zip(sets, outs):
+            assert torch.equal(o, B.attention(*s, k_lens=lens))
+
+
+def test_at_model_sizes():
+    """56 heads of 128, 4097 tokens to 512 and to themselves: sampled heads."""
+    for Lq, Lk in ((4097, 512), (4097, 4097)):
+        q, k, v = inputs(Lq, Lk, 56, 56, 128, 12)
+        got = B.attention(q, k, v)
+        for h in (0, 17, 55):
+            one = [t[:, h:h + 1] for t in (q, k, v)]
+            want, bound, _ = R.attention(*one, R.sequences(Lq, Lk, 1))
+            R.check_bf16(got[:, h:h + 1], want, bound)
+
+
+def test_binding_refuses():
+    q, k, v = inputs(6, 9, 4, 2, 64, 13)
+    o = ints([0, 3, 6])
+    for args, kw in [
+            ((q.float(), k, v), {}), ((q, k.float(), v), {}),
+            ((q, k, v[:8]), {}), ((q, k, v[:, :1]), {}), ((None, k, v), {}),
+            ((q, k[..., :32].contiguous(), v[..., :32].contiguous()), {}),
+            ((q.cpu(), k, v), {}), ((q, k.cpu(), v), {}), ((q[0], k, v), {}),
+            ((q[None], k, v), {}), ((q[None], k[None], v), {}),
+            ((q[None], k[None], v[None]), dict(q_offsets=o)),
+            ((q, k, v), dict(q_offsets=o.long())),
+            ((q, k, v), dict(q_offsets=o[:1])),
+            ((q, k, v), dict(q_offsets=o, k_offsets=ints([0, 9]))),
+            ((q, k, v), dict(q_offsets=o, k_offsets=o, k_lens=ints([9]))),
+            ((q, k, v), dict(out=torch.empty_like(k))),
+            ((q.transpose(0, 1), k, v), {}), ((q, k, v[:, :, ::2]), {})]:
+        with pytest.raises((ValueError, TypeError)):
+            B.attention(*args, **kw)
+    for args, kw in [
+            ((q[:, :3].contiguous(), k, v), {}),      # 3 heads to 2
+            ((q, k, v), dict(k_lens=ints([9, 9]))),   # 9 rows, 2 sequences
+            ((q, k, v), dict(scale=0.0)), ((q, k, v), dict(scale=-1.0)),
+            ((q, k, v), dict(scale=math.inf)), ((q, k, v), dict(scale=NAN)),
+            ((q, k, v), dict(out=q)),
+            ((*(torch.zeros(4, 1, 136, dtype=BF, device="cuda"),) * 3,), {}),
+            ((*(torch.zeros(4, 1, 12, dtype=BF, device="cuda"),) * 3,), {})]:
+        with pytest.raises(B.W8A8Error):
+            B.attention(*args, **kw)
+    q, k, v = inputs(1, 6000, 2, 2, 64, 14)
+    need = B.attention_workspace_bytes(1, 6000, 2, 2, 64)
+    small = torch.empty(need - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(B.W8A8Error):
+        B.attention(q, k, v, workspace=small)

@@ -9,6 +9,7 @@ BF16 tensors are passed as their bit patterns (the library's uint16 BF16).
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -27,6 +28,9 @@ GLUE_MAX_K = 90112   # SiLU, renormalization and the fused quantizers
 NORM_MAX_H = 32768   # block norms
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 W4_GROUPS = (32, 64, 128)
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_MAX_AXES = 4
+ROPE_MAX_PAIRS = 256
 
 
 class _Norm(ctypes.Structure):  # w8a8_norm_t
@@ -42,10 +46,37 @@ class _Modulation(ctypes.Structure):  # w8a8_modulation_t
                 ("row", ctypes.c_void_p)]
 
 
+class _Rope(ctypes.Structure):  # w8a8_rope_t
+    _fields_ = [("axes", ctypes.c_int), ("pairs", ctypes.c_int * 4),
+                ("scaling", ctypes.c_int), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class _Heads(ctypes.Structure):  # w8a8_heads_t
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("heads", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("norm", _Norm),
+                ("per_head", ctypes.c_int)]
+
+
+class _Attention(ctypes.Structure):  # w8a8_attention_t
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out")] +
+                [(n, ctypes.c_int64) for n in (
+                    "q_stride", "k_stride", "v_stride", "out_stride", "Tq",
+                    "Tk", "B", "q_heads", "k_heads", "D")] +
+                [(n, ctypes.c_void_p) for n in (
+                    "q_offsets", "k_offsets", "k_lens")] +
+                [("scale", ctypes.c_float)])
+
+
 # Every symbol include/w8a8.h declares, with its ctypes signature.
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 _F = ctypes.c_float
 _PN, _PM = ctypes.POINTER(_Norm), ctypes.POINTER(_Modulation)
+_PH, _PA = ctypes.POINTER(_Heads), ctypes.POINTER(_Attention)
 SIGNATURES = {
     "w8a8_quantize_act": (_I, [_P, _I64, _I64, _P, _P, _P]),
     "w8a8_quantize_act_silu": (_I, [_P, _I64, _I64, _P, _P, _P]),
@@ -78,6 +109,11 @@ SIGNATURES = {
     "w8a8_w4_quantize_weight": (_I, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "w8a8_w4_pack_weight": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P]),
     "w8a8_w4_linear": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]),
+    "w8a8_rope_table": (_I, [_P, _I, _I64, ctypes.POINTER(_Rope), _P, _P]),
+    "w8a8_head_norm_rope": (_I, [_PH, _PH, _I64, _I64, _P, _I64, _I64, _P, _I,
+                                 _P]),
+    "w8a8_attention_workspace_bytes": (_SZ, [_PA]),
+    "w8a8_attention": (_I, [_PA, _P, _SZ, _P]),
 }
 
 
@@ -770,3 +806,280 @@ def w4_linear(x, w4, w4_scale, bias=None, *, out=None, stream=None):
         128 // parts, _stream(stream)))
     _on_stream(stream, out if own_out else None)
     return out
+
+
+# ---------------------------------------------------------------------------
+# heads: rotary table, head norms with rotation, attention
+# ---------------------------------------------------------------------------
+
+def rope_table(positions, pairs, *, theta=10000.0, scaling="none", factor=1.0,
+               original=0.0, beta_fast=32.0, beta_slow=1.0, amplitude=None,
+               out=None, stream=None):
+    """positions: int32 or float32 [T] or [T, axes] -> float32 [T, 2, P], the
+    cosines and sines of P = sum(pairs) pairs a token.
+
+    pairs: how many pairs each axis turns (a number for one axis).  scaling:
+    "none", "linear", "ntk" or "yarn" (the last with `original`, the number of
+    positions that the unscaled rotation was made for, and an amplitude of
+    0.1 ln(factor) + 1 unless given)."""
+    torch = _torch()
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    kind = {torch.int32: 0, torch.float32: 1}.get(positions.dtype)
+    if kind is None:
+        raise ValueError(f"positions: expected int32 or float32, got "
+                         f"{positions.dtype}")
+    pairs = (pairs,) if isinstance(pairs, int) else tuple(pairs)
+    if not 1 <= len(pairs) <= ROPE_MAX_AXES or min(pairs) < 1 or \
+            sum(pairs) > ROPE_MAX_PAIRS:
+        raise ValueError(f"pairs: expected 1 to {ROPE_MAX_AXES} axes of 1 or "
+                         f"more pairs, {ROPE_MAX_PAIRS} in all, got {pairs}")
+    if positions.dim() == 1 and len(pairs) == 1:
+        _need(positions, positions.dtype, 1, "positions")
+    else:
+        _need(positions, positions.dtype, 2, "positions",
+              (positions.shape[0] if positions.dim() else 0, len(pairs)))
+    code = ROPE_SCALINGS.get(scaling)
+    if code is None:
+        raise ValueError(f"scaling: expected one of {sorted(ROPE_SCALINGS)}, "
+                         f"got {scaling!r}")
+    if amplitude is None:
+        amplitude = (0.1 * math.log(factor) + 1
+                     if scaling == "yarn" and factor > 1 else 1.0)
+    T, P = positions.shape[0], sum(pairs)
+    own_out = out is None
+    if own_out:
+        out = torch.empty((T, 2, P), dtype=torch.float32,
+                          device=positions.device)
+    else:
+        _need(out, torch.float32, 3, "out", (T, 2, P))
+    rope = _Rope(len(pairs), (ctypes.c_int * 4)(*pairs), code, theta, factor,
+                 original, beta_fast, beta_slow, amplitude)
+    _check("w8a8_rope_table", lib().w8a8_rope_table(
+        _ptr(positions), kind, T, rope, _ptr(out), _stream(stream)))
+    _on_stream(stream, out if own_out else None)
+    return out
+
+
+def _head_rows(t, name, shape=None):
+    """t: bf16 [T, heads, D], the heads of a token behind each other, tokens at
+    any stride (a part of a fused output's columns) -> that stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    size, step = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or len(size) != 3 or \
+            (size[2] > 1 and step[2] != 1) or \
+            (size[1] > 1 and step[1] != size[2]):
+        raise ValueError(f"{name}: expected {torch.bfloat16} [tokens, heads, "
+                         f"width] with the heads of a token behind each "
+                         f"other, got {t.dtype} {tuple(size)} with strides "
+                         f"{step}")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got "
+                         f"{tuple(size)}")
+    _on_current_gpu(t, name)
+    return step[0] if size[0] > 1 else size[1] * size[2]
+
+
+def _heads_arg(x, y, kind, weight, bias, eps, name):
+    """A w8a8_heads_t; the vectors must outlive the call."""
+    stride = _head_rows(x, name)
+    H, D = x.shape[1:]
+    y_stride = _head_rows(y, f"{name}'s output", x.shape)
+    bf16 = _torch().bfloat16
+    per_head, ptr = None, [None, None]
+    for i, (t, what) in enumerate(((weight, "weight"), (bias, "bias"))):
+        if t is None:
+            continue
+        full = t.dim() == 2
+        if full and H == 1:
+            full = False
+            t = t[0]
+        _need(t, bf16, 2 if full else 1, f"{name} {what}",
+              (H, D) if full else (D,))
+        if per_head is not None and per_head != full:
+            raise ValueError(f"{name}: weight and bias must both be [{D}] or "
+                             f"both [{H}, {D}]")
+        per_head, ptr[i] = full, t.data_ptr()
+    return _Heads(x.data_ptr(), y.data_ptr(), H, stride, y_stride,
+                  _Norm(kind, eps, *ptr), bool(per_head))
+
+
+def _table_args(M, table, row):
+    """(table, pairs, rows, row) of a rotation."""
+    if table is None:
+        if row is not None:
+            raise ValueError("row needs a table")
+        return None, 0, 0, None
+    torch = _torch()
+    _need(table, torch.float32, 3, "table")
+    rows, two, pairs = table.shape
+    if two != 2:
+        raise ValueError(f"table: expected [rows, 2, pairs], got "
+                         f"{tuple(table.shape)}")
+    if row is not None:
+        _need(row, torch.int32, 1, "row", (M,))
+    elif rows != 1 and rows != M:
+        raise ValueError(f"a table of {rows} rows for {M} tokens needs row")
+    return table.data_ptr(), pairs, rows, _ptr(row)
+
+
+def head_norm_rope(q, k=None, *, norm="rms", q_weight=None, q_bias=None,
+                   k_weight=None, k_bias=None, eps=1e-6, table=None, row=None,
+                   interleaved=False, out=None, stream=None):
+    """Each head's norm, then its rotation by the token's row of a rope_table:
+    q bf16 [M, heads, D] (and k [M, k_heads, D]) -> the same shapes, as a pair
+    where k is given.
+
+    Tokens may lie at any stride (parts of a fused Q, K, V output).  norm:
+    "rms", "layer" or "none"; weights and biases bf16 [D] or [heads, D].  table:
+    float32 [rows, 2, pairs], turning the first 2 pairs values of a head: values
+    i and i + pairs, or 2 i and 2 i + 1 (interleaved); row m is token m's, or
+    row[m] (int32 [M]; outside the table: padding, zeros).  out: a tensor (a
+    pair with k), which may be the inputs."""
+    torch = _torch()
+    code = NORM_KINDS.get(norm)
+    if code is None:
+        raise ValueError(f"norm: expected one of {sorted(NORM_KINDS)}, got "
+                         f"{norm!r}")
+    for t, name in ((q, "q"), (k, "k")):
+        if not isinstance(t, torch.Tensor) and (name == "q" or t is not None):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    own_out = out is None
+    if k is None:
+        if k_weight is not None or k_bias is not None:
+            raise ValueError("k_weight and k_bias need k")
+        outs = (torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+                if own_out else out,)
+    else:
+        if own_out:
+            outs = tuple(torch.empty(t.shape, dtype=torch.bfloat16,
+                                     device=t.device) for t in (q, k))
+        else:
+            outs = tuple(out)
+            if len(outs) != 2:
+                raise ValueError("out: expected a pair, for q and for k")
+    sides = [_heads_arg(q, outs[0], code, q_weight, q_bias, eps, "q")]
+    M, _, D = q.shape
+    if k is not None:
+        sides.append(_heads_arg(k, outs[1], code, k_weight, k_bias, eps, "k"))
+        if k.shape[0] != M or k.shape[2] != D:
+            raise ValueError(f"q and k disagree: {tuple(q.shape)}, "
+                             f"{tuple(k.shape)}")
+    rot = _table_args(M, table, row)
+    _check("w8a8_head_norm_rope", lib().w8a8_head_norm_rope(
+        sides[0], sides[1] if k is not None else None, M, D, *rot,
+        bool(interleaved), _stream(stream)))
+    if own_out:
+        _on_stream(stream, *outs)
+    return outs[0] if k is None else outs
+
+
+def rope(x, table, *, row=None, interleaved=False, out=None, stream=None):
+    """The rotation alone: x bf16 [M, heads, D] -> the same (head_norm_rope
+    without a norm)."""
+    if table is None:
+        raise ValueError("rope needs a table")
+    return head_norm_rope(x, norm="none", table=table, row=row,
+                          interleaved=interleaved, out=out, stream=stream)
+
+
+def _flat_batch(t, name):
+    """[B, L, heads, D] -> [B L, heads, D]; anything else as it is."""
+    if isinstance(t, _torch().Tensor) and t.dim() == 4:
+        if t.shape[0] > 1 and t.shape[1] > 1 and \
+                t.stride(0) != t.shape[1] * t.stride(1):
+            raise ValueError(f"{name}: the batch's sequences must follow each "
+                             f"other, got strides {t.stride()}")
+        if t.shape[1] == 1:
+            return t[:, 0]
+        return t.as_strided((t.shape[0] * t.shape[1], *t.shape[2:]),
+                            t.stride()[1:])
+    return t
+
+
+def _attention_arg(q, k, v, out, scale, q_offsets, k_offsets, k_lens):
+    torch = _torch()
+    B = None
+    if isinstance(q, torch.Tensor) and q.dim() == 4:
+        if q_offsets is not None or k_offsets is not None:
+            raise ValueError("offsets go with [tokens, heads, width]")
+        B = q.shape[0]
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4 or \
+                    t.shape[0] != B:
+                raise ValueError(f"{name}: expected [{B}, tokens, heads, "
+                                 "width] like q")
+        if out.shape != q.shape:
+            raise ValueError(f"out: expected shape {tuple(q.shape)}, got "
+                             f"{tuple(out.shape)}")
+    q, k, v, out = (_flat_batch(t, n) for t, n in (
+        (q, "q"), (k, "k"), (v, "v"), (out, "out")))
+    strides = [_head_rows(q, "q"), _head_rows(k, "k"),
+               _head_rows(v, "v", k.shape), _head_rows(out, "out", q.shape)]
+    if k.shape[2] != q.shape[2]:
+        raise ValueError(f"q and k disagree on the head width: "
+                         f"{q.shape[2]}, {k.shape[2]}")
+    for t, name in ((q_offsets, "q_offsets"), (k_offsets, "k_offsets")):
+        if t is None:
+            continue
+        _need(t, torch.int32, 1, name)
+        if t.shape[0] < 2 or (B is not None and t.shape[0] != B + 1):
+            raise ValueError(f"{name}: expected "
+                             f"{'two or more' if B is None else B + 1} "
+                             f"offsets, got {t.shape[0]}")
+        B = t.shape[0] - 1
+    if k_lens is not None:
+        _need(k_lens, torch.int32, 1, "k_lens", None if B is None else (B,))
+        B = k_lens.shape[0]
+    B = 1 if B is None else B
+    D = q.shape[2]
+    if scale is None:
+        scale = 1 / math.sqrt(D) if D else 1.0
+    return _Attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *strides,
+        q.shape[0], k.shape[0], B, q.shape[1], k.shape[1], D, _ptr(q_offsets),
+        _ptr(k_offsets), _ptr(k_lens), scale)
+
+
+def attention(q, k, v, *, scale=None, q_offsets=None, k_offsets=None,
+              k_lens=None, out=None, workspace=None, stream=None):
+    """softmax(scale q k^T) v per head, over all keys of a sequence (scale: 1 /
+    sqrt(width) unless given).
+
+    q: bf16 [Tq, heads, D]; k, v: [Tk, k_heads, D], k_heads dividing heads (a
+    group of query heads shares a key head); tokens at any stride.  One
+    sequence, or several: packed behind each other with q_offsets and k_offsets
+    (int32 [B + 1]; None: equal lengths), or as a batch q [B, Lq, heads, D], k
+    and v [B, Lk, k_heads, D].  k_lens (int32 [B]): how many of a sequence's
+    keys count.  Returns bf16 of q's shape; rows outside of all sequences are
+    not written, those of a sequence without keys are zero.  workspace:
+    attention_workspace_bytes of uint8, of this call alone while it runs."""
+    torch = _torch()
+    own_out = out is None
+    if own_out:
+        if not isinstance(q, torch.Tensor):
+            raise TypeError("q must be a torch.Tensor")
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    a = _attention_arg(q, k, v, out, scale, q_offsets, k_offsets, k_lens)
+    L = lib()
+    ws = _workspace(int(L.w8a8_attention_workspace_bytes(a)), q.device,
+                    workspace)
+    ws_len = 0 if ws is None else ws.numel() * ws.element_size()
+    _check("w8a8_attention", L.w8a8_attention(a, _ptr(ws), ws_len,
+                                              _stream(stream)))
+    _on_stream(stream, out if own_out else None,
+               ws if workspace is None else None)
+    return out
+
+
+def attention_workspace_bytes(Tq, Tk, heads, k_heads, D, *, B=1,
+                              packed=False):
+    """Bytes attention() needs for B sequences of Tq query and Tk key rows in
+    all; packed: with q_offsets."""
+    a = _Attention(Tq=Tq, Tk=Tk, B=B, q_heads=heads, k_heads=k_heads, D=D,
+                   q_stride=heads * D, k_stride=k_heads * D,
+                   v_stride=k_heads * D, out_stride=heads * D, scale=1.0,
+                   q_offsets=4 if packed else None, k_offsets=4)
+    return int(lib().w8a8_attention_workspace_bytes(a))

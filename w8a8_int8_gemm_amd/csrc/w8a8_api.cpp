@@ -12,6 +12,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "heads.h"
 #include "internal.h"
 #include "norm.h"
 #include "rowwise.h"
@@ -304,6 +305,103 @@ int validate_w4(int64_t N, int64_t K, int64_t group) {
       K % 128 != 0 || K > W8A8_MAX_K || N * K >= (int64_t(1) << 37))
     return W8A8_ERR_SHAPE;
   if (group != 32 && group != 64 && group != 128) return W8A8_ERR_ARG;
+  return W8A8_OK;
+}
+
+// Rows of `width` elements at a stride (both in 2-byte elements).
+struct Rows {
+  const void *p;
+  int64_t rows, width, stride;
+};
+
+Range range_of(const Rows &r) {
+  return range_of(r.p, r.p ? ((r.rows - 1) * r.stride + r.width) * 2 : 0);
+}
+
+// Whether two sets of rows share an element: they do not where their spans are
+// apart, or where they lie at one stride and the parts of a row are apart.
+bool overlap(const Rows &a, const Rows &b) {
+  const Range ra = range_of(a), rb = range_of(b);
+  if (!overlap(ra, rb)) return false;
+  if (a.stride != b.stride || (a.rows == 1 && b.rows == 1)) return true;
+  const int64_t step = a.stride * 2;
+  int64_t ahead = ((int64_t)rb.lo - (int64_t)ra.lo) % step;
+  if (ahead < 0) ahead += step;
+  return ahead < a.width * 2 || step - ahead < b.width * 2;
+}
+
+bool stride_ok(int64_t stride, int64_t width, int64_t limit) {
+  return stride >= width && stride % 8 == 0 && stride < limit;
+}
+
+// One side of the head norms.
+int validate_heads(const w8a8_heads_t *h, int64_t M, int64_t D) {
+  if (!h->x || !h->y) return W8A8_ERR_NULL;
+  if (h->heads < 1 || h->heads > 4096 || M * h->heads * D >= int64_t(1) << 36)
+    return W8A8_ERR_SHAPE;
+  if (!stride_ok(h->x_stride, h->heads * D, kMaxModStride) ||
+      !stride_ok(h->y_stride, h->heads * D, kMaxModStride))
+    return W8A8_ERR_SHAPE;
+  const int st = validate_norm(&h->norm);
+  if (st != W8A8_OK) return st;
+  return aligned(h->x, 16) && aligned(h->y, 16) ? W8A8_OK : W8A8_ERR_ALIGN;
+}
+
+// Quarter turns a position of pair i of an axis of p pairs.
+double rope_quarters(const w8a8_rope_t &r, int p, int i) {
+  const double pi = 3.14159265358979323846;
+  double theta = r.theta;
+  if (r.scaling == W8A8_ROPE_NTK && p > 1)
+    theta *= std::pow(r.factor, (double)p / (p - 1));
+  double f = std::pow(theta, -(double)i / p);
+  if (r.scaling == W8A8_ROPE_LINEAR) f /= r.factor;
+  if (r.scaling == W8A8_ROPE_YARN) {
+    auto at = [&](double turns) {
+      return p * std::log(r.original / (2 * pi * turns)) / std::log(r.theta);
+    };
+    const double low = std::fmax(std::floor(at(r.beta_fast)), 0.0);
+    const double high = std::fmin(std::ceil(at(r.beta_slow)), 2.0 * p - 1);
+    const double span = std::fmax(high - low, 0.001);
+    const double ramp = std::fmin(std::fmax((i - low) / span, 0.0), 1.0);
+    f = f / r.factor * ramp + f * (1 - ramp);
+  }
+  return f * (2 / pi);
+}
+
+bool positive(double v) { return v > 0 && std::isfinite(v); }
+
+// Everything of an attention call but its workspace and device; `args` and
+// `plan` are filled in.
+int validate_attention(const w8a8_attention_t *a, w8a8::AttnArgs *args,
+                       w8a8::AttnPlan *plan) {
+  const int64_t most = int64_t(1) << 31;
+  if (!a) return W8A8_ERR_NULL;
+  if (a->B < 1 || a->B > 1 << 20 || a->Tq < 1 || a->Tk < 0 || a->D < 8 ||
+      a->D > 128 || a->D % 8 != 0 || a->q_heads < 1 || a->k_heads < 1 ||
+      a->q_heads >= most || a->q_heads % a->k_heads != 0 || a->Tq >= most ||
+      a->Tk >= most || a->Tq * a->q_heads >= most ||
+      a->Tk * a->k_heads >= most)
+    return W8A8_ERR_SHAPE;
+  if ((!a->q_offsets && a->Tq % a->B != 0) ||
+      (!a->k_offsets && a->Tk % a->B != 0))
+    return W8A8_ERR_SHAPE;
+  const int64_t wq = a->q_heads * a->D, wk = a->k_heads * a->D;
+  const int64_t limit = int64_t(1) << 22;
+  if (!stride_ok(a->q_stride, wq, limit) ||
+      !stride_ok(a->out_stride, wq, limit) ||
+      !stride_ok(a->k_stride, wk, limit) || !stride_ok(a->v_stride, wk, limit))
+    return W8A8_ERR_SHAPE;
+  if (!(a->scale > 0) || !std::isfinite(a->scale)) return W8A8_ERR_ARG;
+  *plan = w8a8::plan_attention(a->Tq, a->Tk, a->B, a->q_offsets != nullptr,
+                               a->q_heads, a->k_heads, a->D);
+  if (!w8a8::attention_launchable(*plan, a->k_heads)) return W8A8_ERR_SHAPE;
+  *args = w8a8::AttnArgs{
+      a->q,        a->k,        a->v,      a->out,
+      a->q_stride, a->k_stride, a->v_stride, a->out_stride,
+      a->q_offsets, a->k_offsets, a->k_lens,
+      (int)a->Tq,  (int)a->Tk,  (int)a->B, (int)a->q_heads,
+      (int)a->k_heads, (int)a->D,
+      (float)(a->scale * 1.44269504088896340736), nullptr};
   return W8A8_OK;
 }
 
@@ -653,6 +751,167 @@ int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
   return hip_status(w8a8::launch_w4_linear(
       x, w4, w4_scale, bias, y, M, N, K, (int)group,
       static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_rope_table(const void *positions, int position_type, int64_t T,
+                    const w8a8_rope_t *rope, float *table, void *stream) {
+  if (!positions || !rope || !table) return W8A8_ERR_NULL;
+  if (T < 1 || T > kMaxTokenRows || rope->axes < 1 ||
+      rope->axes > W8A8_ROPE_MAX_AXES)
+    return W8A8_ERR_SHAPE;
+  int64_t pairs = 0;
+  for (int i = 0; i < rope->axes; ++i) {
+    if (rope->pairs[i] < 1) return W8A8_ERR_SHAPE;
+    pairs += rope->pairs[i];
+  }
+  if (pairs > W8A8_ROPE_MAX_PAIRS) return W8A8_ERR_SHAPE;
+  if (position_type != W8A8_POSITIONS_I32 &&
+      position_type != W8A8_POSITIONS_F32)
+    return W8A8_ERR_ARG;
+  const int how = rope->scaling;
+  if (how < W8A8_ROPE_NONE || how > W8A8_ROPE_YARN ||
+      !positive(rope->theta) || rope->theta <= 1 ||
+      !std::isfinite(rope->amplitude))
+    return W8A8_ERR_ARG;
+  if (how != W8A8_ROPE_NONE && (!positive(rope->factor) || rope->factor < 1))
+    return W8A8_ERR_ARG;
+  if (how == W8A8_ROPE_YARN &&
+      (!positive(rope->original) || !positive(rope->beta_fast) ||
+       !positive(rope->beta_slow)))
+    return W8A8_ERR_ARG;
+  if (!aligned(positions, 4) || !aligned(table, 16)) return W8A8_ERR_ALIGN;
+  if (overlap(range_of(positions, T * rope->axes * 4),
+              range_of(table, T * pairs * 8)))
+    return W8A8_ERR_ALIAS;
+  int st = check_device();
+  if (st != W8A8_OK) return st;
+  w8a8::RopeArgs a{};
+  a.pos = positions;
+  a.table = table;
+  a.T = T;
+  a.pos_type = position_type;
+  a.axes = rope->axes;
+  a.pairs = (int)pairs;
+  a.amplitude = (float)rope->amplitude;
+  int at = 0;
+  for (int x = 0; x < rope->axes; ++x)
+    for (int i = 0; i < rope->pairs[x]; ++i, ++at) {
+      a.axis[at] = (uint8_t)x;
+      a.quarters[at] = rope_quarters(*rope, rope->pairs[x], i);
+    }
+  return hip_status(
+      w8a8::launch_rope_table(a, static_cast<hipStream_t>(stream)));
+}
+
+int w8a8_head_norm_rope(const w8a8_heads_t *q, const w8a8_heads_t *k,
+                        int64_t M, int64_t D, const float *table,
+                        int64_t pairs, int64_t rows, const int32_t *row,
+                        int interleaved, void *stream) {
+  if (!q) return W8A8_ERR_NULL;
+  if (M < 1 || M > kMaxTokenRows || D < 8 || D > 256 || D % 8 != 0)
+    return W8A8_ERR_SHAPE;
+  if (table) {
+    if (pairs < 4 || pairs % 4 != 0 || 2 * pairs > D || rows < 1 ||
+        rows > kMaxRows || (!row && rows != 1 && rows != M))
+      return W8A8_ERR_SHAPE;
+    if (!aligned(table, 16) || !aligned(row, 4)) return W8A8_ERR_ALIGN;
+  }
+  const w8a8_heads_t *sides[2] = {q, k};
+  w8a8::HeadArgs a{};
+  Rows in[2], out[2];
+  int n = 0;
+  for (const w8a8_heads_t *h : sides) {
+    if (!h) continue;
+    const int st = validate_heads(h, M, D);
+    if (st != W8A8_OK) return st;
+    a.side[n] = w8a8::HeadSide{h->x, h->y, h->norm.weight, h->norm.bias,
+                               h->x_stride, h->y_stride, (int)h->heads,
+                               h->norm.kind, h->per_head ? (int)D : 0,
+                               h->norm.eps};
+    in[n] = Rows{h->x, M, h->heads * D, h->x_stride};
+    out[n++] = Rows{h->y, M, h->heads * D, h->y_stride};
+  }
+  for (int i = 0; i < n; ++i) {
+    for (int j = 0; j < n; ++j) {
+      const bool same = i == j && out[i].p == in[j].p &&
+                        out[i].stride == in[j].stride;
+      if (!same && overlap(out[i], in[j])) return W8A8_ERR_ALIAS;
+      if (j < i && overlap(out[i], out[j])) return W8A8_ERR_ALIAS;
+      const int64_t vec = (sides[j]->per_head ? sides[j]->heads : 1) * D * 2;
+      const Range ro = range_of(out[i]);
+      for (const uint16_t *p : {a.side[j].weight, a.side[j].bias})
+        if (p && overlap(ro, range_of(p, vec))) return W8A8_ERR_ALIAS;
+    }
+    if (table &&
+        (overlap(range_of(out[i]), range_of(table, rows * pairs * 8)) ||
+         overlap(range_of(out[i]), range_of(row, row ? M * 4 : 0))))
+      return W8A8_ERR_ALIAS;
+  }
+  if (table) {
+    a.table = table;
+    a.row = row;
+    a.rows = (int)rows;
+    a.row_step = rows > 1 ? 1 : 0;
+    a.pairs = (int)pairs;
+    a.interleaved = interleaved != 0;
+  } else {
+    a.rows = 1;
+  }
+  a.M = M;
+  a.D = (int)D;
+  if (w8a8::head_norm_items(a) >= int64_t(1) << 32) return W8A8_ERR_SHAPE;
+  const int st = check_device();
+  if (st != W8A8_OK) return st;
+  return hip_status(
+      w8a8::launch_head_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t w8a8_attention_workspace_bytes(const w8a8_attention_t *a) {
+  w8a8::AttnArgs args;
+  w8a8::AttnPlan plan;
+  return validate_attention(a, &args, &plan) == W8A8_OK ? plan.workspace : 0;
+}
+
+int w8a8_attention(const w8a8_attention_t *a, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+  if (!a || !a->q || !a->out || (a->Tk > 0 && (!a->k || !a->v)))
+    return W8A8_ERR_NULL;
+  w8a8::AttnArgs args;
+  w8a8::AttnPlan plan;
+  int st = validate_attention(a, &args, &plan);
+  if (st != W8A8_OK) return st;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) ||
+      !aligned(a->out, 16) || !aligned(a->q_offsets, 4) ||
+      !aligned(a->k_offsets, 4) || !aligned(a->k_lens, 4))
+    return W8A8_ERR_ALIGN;
+  const int64_t wq = a->q_heads * a->D, wk = a->k_heads * a->D;
+  const Rows out = {a->out, a->Tq, wq, a->out_stride};
+  const Rows ins[] = {{a->q, a->Tq, wq, a->q_stride},
+                      {a->Tk ? a->k : nullptr, a->Tk, wk, a->k_stride},
+                      {a->Tk ? a->v : nullptr, a->Tk, wk, a->v_stride}};
+  const Range lists[] = {
+      range_of(a->q_offsets, a->q_offsets ? (a->B + 1) * 4 : 0),
+      range_of(a->k_offsets, a->k_offsets ? (a->B + 1) * 4 : 0),
+      range_of(a->k_lens, a->k_lens ? a->B * 4 : 0)};
+  for (const Rows &r : ins)
+    if (overlap(out, r)) return W8A8_ERR_ALIAS;
+  for (const Range &r : lists)
+    if (overlap(range_of(out), r)) return W8A8_ERR_ALIAS;
+  if (plan.workspace > 0) {
+    if (!workspace || workspace_bytes < plan.workspace)
+      return W8A8_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return W8A8_ERR_ALIGN;
+    const Range rw = range_of(workspace, (int64_t)plan.workspace);
+    if (overlap(rw, range_of(out))) return W8A8_ERR_ALIAS;
+    for (const Rows &r : ins)
+      if (overlap(rw, range_of(r))) return W8A8_ERR_ALIAS;
+    for (const Range &r : lists)
+      if (overlap(rw, r)) return W8A8_ERR_ALIAS;
+    args.workspace = workspace;
+  }
+  if ((st = check_device()) != W8A8_OK) return st;
+  return hip_status(w8a8::launch_attention(args, plan,
+                                           static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
