@@ -7,9 +7,10 @@ input; the attention output projection and FC1 each quantize their own
 input; FC2 takes SiLU of FC1's BF16 output, quantized ("MLX implementation
 and experiment report", "What the default preserves": SiLU applied to the
 BF16 value, rounded per the original recipe).  Attention and the norms are
-not part of the projection path, so the synthetic block feeds its input X
-to O and FC1 as well; that keeps four quantizations per block, as in the
-model.  Everything here is a sequence of library calls on one stream;
+not part of the projection path, so the synthetic block (``BlockRunner``)
+feeds its input X to O and FC1 as well; that keeps four quantizations per
+block, as in the model.  ``NormedBlock`` has the norms, and the attention
+where its heads are described.  Everything here is a sequence of library calls on one stream;
 outputs and scratch are preallocated once per token count.  The pages' own
 H3 shapes (see datagen) use SwiGLU over a fused gate | up FC1 and feed V's
 output (the attention result's shape) to the attention output projection.
@@ -247,24 +248,71 @@ class BlockNorms:
                     gate=self.table[:, at:at + H])
 
 
+@dataclass
+class BlockHeads:
+    """A block's attention: heads of ``width`` values (as many as Q's and K's
+    outputs hold; several query heads may share a key head), their norms (each
+    vector bf16 [width], [heads, width] or None), the rotation of queries and
+    keys (``table`` float32 [rows, 2, pairs] of ``binding.rope_table``, ``row``
+    int32 [M]) and the sequences (``binding.attention``'s offsets and key
+    lengths; without them all tokens are one sequence, or ``batch`` equal ones).
+    A padding token of the norms is a key like any other unless the offsets or
+    lengths leave it out."""
+    width: int
+    norm: str = "rms"
+    q_weight: object = None
+    k_weight: object = None
+    q_bias: object = None
+    k_bias: object = None
+    eps: float = 1e-6
+    table: object = None
+    row: object = None
+    interleaved: bool = False
+    scale: object = None
+    batch: int = 1
+    q_offsets: object = None
+    k_offsets: object = None
+    k_lens: object = None
+
+
 class NormedBlock:
-    """A whole block without its attention: norm and modulation, Q, K, V, the
-    attention output projection (fed by V's output, the attention result's
-    shape), gate and residual, the next norm, the MLP, gate and residual.
+    """A whole block: norm and modulation, Q, K, V, the attention, its output
+    projection, gate and residual, the next norm, the MLP, gate and residual.
     Buffers are preallocated for one token count.  With ``four_bit`` the
     projections are DeviceProj4 and activations stay BF16 (a few tokens);
-    otherwise DeviceProj, and the norms write INT8 codes."""
+    otherwise DeviceProj, and the norms write INT8 codes.
+
+    ``heads`` describes the attention; without it V's output (the attention
+    result's shape) feeds the output projection.  With ``context_tokens`` the
+    attention is one to other states (an encoder's): K and V read the
+    ``context`` given to ``run``, bf16 [context_tokens, K's inputs], whose keys
+    are normed but not turned."""
 
     def __init__(self, M: int, projs=D.BLOCK_PROJS, mlp: str = "silu",
-                 four_bit: bool = False, device="cuda"):
+                 four_bit: bool = False, device="cuda", heads=None,
+                 context_tokens=None):
         import torch
         self.M, self.mlp, self.four_bit = M, mlp, four_bit
+        self.heads, self.context_tokens = heads, context_tokens
         shape = {p.name: (p.N, p.K) for p in projs}
         H = shape["q"][1]
         bf, i8, f32 = torch.bfloat16, torch.int8, torch.float32
         e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=device)
-        self.out = {n: e(M, N) for n, (N, _) in shape.items()}
+        Mk = M if context_tokens is None else context_tokens
+        self.out = {n: e(Mk if n in ("k", "v") else M, N)
+                    for n, (N, _) in shape.items()}
         self.r = e(M, H)
+        if heads is None:
+            if context_tokens is not None:
+                raise ValueError("context_tokens needs heads")
+        else:
+            if context_tokens is not None and heads.table is not None:
+                raise ValueError("a context's keys are not turned")
+            self.a = e(M, shape["q"][0])
+            self.aws = e(max(B.attention_workspace_bytes(
+                M, Mk, shape["q"][0] // heads.width,
+                shape["k"][0] // heads.width, heads.width, B=self._batch(),
+                packed=heads.q_offsets is not None), 16), dt=torch.uint8)
         if four_bit:
             self.y = e(M, H)
             self.h = e(M, shape["fc2"][1])
@@ -272,16 +320,57 @@ class NormedBlock:
         self.yq, self.ys = e(M, H, dt=i8), e(M, dt=f32)
         self.oq, self.os = e(M, shape["o"][1], dt=i8), e(M, dt=f32)
         self.hq, self.hs = e(M, shape["fc2"][1], dt=i8), e(M, dt=f32)
-        need = max(B.gemm_workspace_bytes(M, N, K) for N, K in shape.values())
+        if context_tokens is not None:
+            self.cq, self.cs = e(Mk, shape["k"][1], dt=i8), e(Mk, dt=f32)
+        need = max(B.gemm_workspace_bytes(m, N, K) for N, K in shape.values()
+                   for m in (M, Mk))
         self.ws = e(max(need, 256), dt=torch.uint8)
 
-    def run(self, x, projs: dict, norms: BlockNorms, out=None, stream=None):
+    def _batch(self) -> int:
+        h = self.heads
+        if h.k_lens is not None:
+            return h.k_lens.shape[0]
+        for o in (h.q_offsets, h.k_offsets):
+            if o is not None:
+                return o.shape[0] - 1
+        return h.batch
+
+    def run(self, x, projs: dict, norms: BlockNorms, out=None, stream=None,
+            context=None):
         """x: bf16 [M, H] -> bf16 [M, H] (``out``, or a new tensor)."""
+        if (context is None) != (self.context_tokens is None):
+            raise ValueError("context goes with context_tokens")
         run = self._run4 if self.four_bit else self._run8
         rows = dict(mod_row=norms.mod_row, stream=stream)
-        return run(x, projs, norms, rows, out, stream)
+        return run(x, projs, norms, rows, out, stream, context)
 
-    def _run8(self, x, projs, norms, rows, out, stream):
+    def _attend(self, stream):
+        """The attention of the block's Q, K, V outputs (queries and keys are
+        normed and turned where they lie), or V's output without heads."""
+        h = self.heads
+        if h is None:
+            return self.out["v"]
+        q, k, v = (self.out[n].unflatten(1, (-1, h.width)) for n in "qkv")
+        shared = dict(norm=h.norm, eps=h.eps, stream=stream)
+        turn = dict(table=h.table, row=h.row, interleaved=h.interleaved)
+        qv = dict(q_weight=h.q_weight, q_bias=h.q_bias)
+        if self.context_tokens is None:
+            if h.norm != "none" or h.table is not None:
+                B.head_norm_rope(q, k, k_weight=h.k_weight, k_bias=h.k_bias,
+                                 out=(q, k), **qv, **shared, **turn)
+        elif h.norm != "none":
+            B.head_norm_rope(q, out=q, **qv, **shared)
+            B.head_norm_rope(k, q_weight=h.k_weight, q_bias=h.k_bias, out=k,
+                             **shared)
+        a = self.a.unflatten(1, (-1, h.width))
+        if h.batch > 1 and h.q_offsets is None and h.k_offsets is None:
+            q, k, v, a = (t.unflatten(0, (h.batch, -1)) for t in (q, k, v, a))
+        B.attention(q, k, v, scale=h.scale, q_offsets=h.q_offsets,
+                    k_offsets=h.k_offsets, k_lens=h.k_lens, out=a,
+                    workspace=self.aws, stream=stream)
+        return self.a
+
+    def _run8(self, x, projs, norms, rows, out, stream, context):
         def gemm(name, q, s):
             p = projs[name]
             B.gemm(q, s, p.w, p.sw, p.bias, out=self.out[name],
@@ -289,9 +378,14 @@ class NormedBlock:
 
         y = (self.yq, self.ys)
         B.norm_modulate_quantize(x, **norms.before(0), **rows, out=y)
+        keys = y
+        if context is not None:
+            keys = (self.cq, self.cs)
+            B.quantize_act(context, out=keys, stream=stream)
         for n in ("q", "k", "v"):
-            gemm(n, *y)
-        B.quantize_act(self.out["v"], out=(self.oq, self.os), stream=stream)
+            gemm(n, *(y if n == "q" else keys))
+        B.quantize_act(self._attend(stream), out=(self.oq, self.os),
+                       stream=stream)
         gemm("o", self.oq, self.os)
         B.gated_residual_norm_quantize(
             x, self.out["o"], **norms.behind(0), **norms.before(1), **rows,
@@ -306,7 +400,7 @@ class NormedBlock:
         return B.gated_residual(self.r, self.out["fc2"], **norms.behind(1),
                                 **rows, out=out)
 
-    def _run4(self, x, projs, norms, rows, out, stream):
+    def _run4(self, x, projs, norms, rows, out, stream, context):
         def linear(name, a):
             p = projs[name]
             B.w4_linear(a, p.w4, p.w4_scale, p.bias, out=self.out[name],
@@ -314,8 +408,8 @@ class NormedBlock:
 
         B.norm_modulate(x, **norms.before(0), **rows, out=self.y)
         for n in ("q", "k", "v"):
-            linear(n, self.y)
-        linear("o", self.out["v"])
+            linear(n, self.y if n == "q" or context is None else context)
+        linear("o", self._attend(stream))
         B.gated_residual_norm(x, self.out["o"], **norms.behind(0),
                               **norms.before(1), **rows,
                               out=(self.r, self.y))
