@@ -49,12 +49,17 @@ struct Cfg {
   static constexpr int NO = DP / 32;             // output tiles
   static constexpr int SIDE = KT * RB;           // bytes of a stage's K (or V)
   static constexpr int STAGE = 2 * SIDE;
-  static constexpr int LOADS = SIDE / 16 / THREADS;  // of K a thread and stage
+  static constexpr int LOADS = (SIDE / 16 + THREADS - 1) / THREADS;
+                                                   // of K a thread and stage
   static constexpr int OROW = DP + 4;            // floats of a joined row
   static constexpr int JOIN = (WK > 1 ? WK * TM * OROW * 4 : TM * OROW * 2) +
                               2 * WK * TM * 4;
   static constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
-  static_assert(LDS <= 160 * 1024 && SIDE % (16 * THREADS) == 0, "");
+  // Work groups a compute unit holds (of waves a SIMD, of LDS).
+  static constexpr int GROUPS = WAVES == 4 ? 2 : 1;
+  static constexpr int AHEAD = KS * NS < 4 ? 2 : 4;
+  static constexpr int WAVES_PER_SIMD = GROUPS * WAVES / 4;
+  static_assert(LDS <= 160 * 1024, "");
 };
 
 // Where chunk c of row r lies in its row: fragments are read by 8 lanes a cycle
@@ -90,23 +95,50 @@ __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Uniform 64-bit address -> buffer resource of `bytes` bytes: reads past them
-// give zeros, in LDS too.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p,
-                                                       uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
-  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(uintptr_t)((hi << 32) | lo), 0,
-      __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+// Uniform 64-bit address -> raw buffer resource of `bytes` bytes: reads past
+// them give zeros, in LDS too.
+__device__ __forceinline__ v4u rsrc(uint64_t at, uint32_t bytes) {
+  return v4u{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (uint64_t)hi << 32 | lo;
 }
 
 // 16 bytes per lane from buffer `r` at byte voff into LDS at `l` (lane i's bytes
-// at l + 16 i).
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, int voff,
-                                           char *l) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)l, 16, voff, 0, 0, 0);
+// at l + 16 i).  Written out because the compiler, which knows only that the
+// builtin writes LDS, waits for every such load before the next transposing
+// read; the waits here are the kernel's own.
+__device__ __forceinline__ void load_lds16(v4u r, int voff, uint32_t l) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(l), "v"(voff), "s"(r)
+      : "memory", "m0");
+}
+
+// A uniform place in LDS, as a number.  Worked out on the spot: the places of all
+// loads of a loop, held over it, would take the scalar registers that the
+// scheduler needs.
+__device__ __forceinline__ uint32_t lds_at(const char *l) {
+  uint32_t v = __builtin_amdgcn_readfirstlane(
+      (int)(uint32_t)(uintptr_t)(lds_void *)l);
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// The same for stores; what lies past the end is not written.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rsrc(uint64_t at,
+                                                           uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)at, 0, bytes,
+                                           0x00020000);
+}
+
+__device__ __forceinline__ void store16(v4u v, __amdgpu_buffer_rsrc_t r,
+                                        int voff) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 0);
 }
 
 // Of a block of 4 rows x 16 values (a lane's 8 bytes at `l`: 4 values of row
@@ -130,33 +162,41 @@ __device__ __forceinline__ int clamped(int v, int lo, int hi) {
   return min(max(v, lo), hi);
 }
 
-__device__ __forceinline__ void keys_of(const AttnArgs &a, int b, Tile &t) {
+// `Args`: AttnArgs, held or read again.
+template <class Args>
+__device__ __forceinline__ Tile tile_of(Args &a, int b, int q0, int nq,
+                                        int row0) {
+  int key0 = 0, keys = a.Tk;
   if (a.k_offsets) {
-    t.key0 = clamped(a.k_offsets[b], 0, a.Tk);
-    t.keys = clamped(a.k_offsets[b + 1], t.key0, a.Tk) - t.key0;
-  } else {
-    t.keys = a.Tk / a.B;
-    t.key0 = b * t.keys;
+    key0 = clamped(a.k_offsets[b], 0, a.Tk);
+    keys = clamped(a.k_offsets[b + 1], key0, a.Tk) - key0;
+  } else if (a.B > 1) {
+    keys = (uint32_t)a.Tk / (uint32_t)a.B;
+    key0 = b * keys;
   }
-  if (a.k_lens) t.keys = clamped(a.k_lens[b], 0, t.keys);
+  if (a.k_lens) keys = clamped(a.k_lens[b], 0, keys);
+  return Tile{q0, nq, key0, keys, row0};
 }
 
-// Tile `i` of all sequences, TM rows each; false past the last.  Offsets are
-// clamped to the rows there are, so no content of theirs leads outside.
-template <int TM>
-__device__ __forceinline__ bool find_tile(const AttnArgs &a, int64_t i,
-                                          Tile &t) {
-  const int G = a.Hq / a.Hk;
-  if (!a.q_offsets) {
-    t.nq = a.Tq / a.B;
-    const int64_t per = ((int64_t)t.nq * G + TM - 1) / TM;
-    const int b = (int)(i / per);
-    t.q0 = b * t.nq;
-    t.row0 = (int)(i - b * per) * TM;
-    if (b >= a.B) return false;
-    keys_of(a, b, t);
-    return true;
+// Tile `i` of sequences of equal lengths, TM rows each.
+template <int TM, class Args>
+__device__ __forceinline__ Tile find_equal_tile(Args &a, uint32_t i) {
+  uint32_t b = 0, nq = a.Tq;
+  if (a.B > 1) {
+    nq = (uint32_t)a.Tq / (uint32_t)a.B;
+    const uint32_t per = (nq * a.G + TM - 1) / TM;
+    b = i / per;
+    i -= b * per;
   }
+  return tile_of(a, b, b * nq, nq, i * TM);
+}
+
+// Tile `i` of all sequences; nq 0 past the last.  Offsets are clamped to the
+// rows there are, so no content of theirs leads outside.
+template <int TM>
+__device__ __forceinline__ Tile find_tile(const AttnArgs &a, uint32_t i) {
+  if (!a.q_offsets) return find_equal_tile<TM>(a, i);
+  const int G = a.G;
   // 64 sequences at a time: their tile counts summed over the lanes.
   const int lane = threadIdx.x & 63;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -166,7 +206,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int64_t i,
       q0 = clamped(a.q_offsets[b], 0, a.Tq);
       nq = clamped(a.q_offsets[b + 1], q0, a.Tq) - q0;
     }
-    const int mine = (int)(((int64_t)nq * G + TM - 1) / TM);
+    const int mine = ((uint32_t)(nq * G) + TM - 1) / TM;
     int upto = mine;
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) {
@@ -174,20 +214,38 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int64_t i,
       if (lane >= s) upto += o;
     }
     const int total = __builtin_amdgcn_readlane(upto, 63);
-    if (i < total) {
-      const uint64_t past = __ballot(upto > (int)i);
-      const int at = __builtin_ctzll(past);
-      t.q0 = __builtin_amdgcn_readlane(q0, at);
-      t.nq = __builtin_amdgcn_readlane(nq, at);
-      t.row0 = ((int)i - (__builtin_amdgcn_readlane(upto, at) -
-                          __builtin_amdgcn_readlane(mine, at))) * TM;
-      keys_of(a, b0 + at, t);
-      return true;
+    if ((int)i < total) {
+      const int at = __builtin_ctzll(__ballot(upto > (int)i));
+      return tile_of(a, b0 + at, __builtin_amdgcn_readlane(q0, at),
+                     __builtin_amdgcn_readlane(nq, at),
+                     ((int)i - (__builtin_amdgcn_readlane(upto, at) -
+                                __builtin_amdgcn_readlane(mine, at))) * TM);
     }
     i -= total;
   }
-  return false;
+  return Tile{0, 0, 0, 0, 0};
 }
+
+// Row r of a tile (r below 2^9): its token and its head among the G that share
+// keys.  x = row0 mod G + r is below 2^20 (G is, by the strides' limit), and (x +
+// 1/2) / G lies 1 / (2 G) or more off every whole number, further than two
+// binary32 roundings of it.
+struct RowMap {
+  int tok0, rem, G;
+  float inv;
+
+  __device__ __forceinline__ RowMap(const Tile &t, int G_) : G(G_) {
+    tok0 = t.q0 + (G == 1 ? t.row0 : t.row0 / G);
+    rem = G == 1 ? 0 : t.row0 % G;
+    inv = 1.0f / (float)G;
+  }
+  __device__ __forceinline__ int past(int r) const {  // tokens past tok0
+    return (int)(((float)(rem + r) + 0.5f) * inv);
+  }
+  __device__ __forceinline__ int head(int r, int past) const {
+    return rem + r - past * G;
+  }
+};
 
 // The larger / the sum of a lane's value and that of the lane 32 further.
 __device__ __forceinline__ float max_halves(float v) {
@@ -222,129 +280,72 @@ __device__ __forceinline__ float2 *part_ml(const AttnArgs &a, int splits,
          (int64_t)split * a.Tq * a.Hq;
 }
 
+// What a wave holds of its 32 query rows (a lane's row: lane % 32, the lane 32
+// further the same), and a stage's work on them.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void attention_kernel(AttnArgs a,
-                                                               int splits) {
-  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wq = wave / C::WK, wk = wave % C::WK;
-  const int half = lane >> 5;
+struct Rows {
+  v8bf fq[C::KS];    // Q^T as the right operand: 8 values a step
+  int ak[C::KS / 2]; // places of the fragments of K and of V^T in a stage
+  int av[C::NO];
+  v16f o[C::NO];
+  // c m (0 until a score sets it), the c s that moves it, and l.
+  float cm, limit, l;
 
-  // Work groups of one head run on one XCD, whose L2 then holds its keys.
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t per_head = gridDim.x / a.Hk;
-  const int kvh = (int)(id / per_head);
-  const int64_t rest = id - kvh * per_head;
-  const int split = (int)(rest % splits);
-  Tile t;
-  if (!find_tile<C::TM>(a, rest / splits, t)) return;
-  const int G = a.Hq / a.Hk;
-  const int rows = min((int64_t)t.nq * G - t.row0, (int64_t)C::TM);
-  const int stages_all = (t.keys + C::KT - 1) / C::KT;
-  const int st0 = (int)((int64_t)split * stages_all / splits);
-  const int st1 = (int)((int64_t)(split + 1) * stages_all / splits);
-
-  // Query row r of the tile: token and head of its sequence's row.
-  auto token = [&](int r) { return t.q0 + (t.row0 + r) / G; };
-  auto head = [&](int r) { return kvh * G + (t.row0 + r) % G; };
-
-  // Q^T as the right operand: lane's query, 8 values a step.
-  v8bf fq[C::KS];
-  {
-    const int r = min(wq * 32 + (lane & 31), rows - 1);
-    const uint16_t *q =
-        a.q + (int64_t)token(r) * a.q_stride + (int64_t)head(r) * a.D;
-#pragma unroll
-    for (int s = 0; s < C::KS; ++s) {
-      const int d = 16 * s + 8 * half;
-      v4u v = {0, 0, 0, 0};
-      if (d < a.D) v = *reinterpret_cast<const v4u *>(q + d);
-      fq[s] = __builtin_bit_cast(v8bf, v);
-    }
-  }
-
-  // Direct loads: what lands in this thread's 16 bytes of a stage.
-  int ok[C::LOADS], ov[C::LOADS];
-  const int ks2 = (int)(a.k_stride * 2), vs2 = (int)(a.v_stride * 2);
-  constexpr int kNowhere = 0x7FFFFFF0;
-#pragma unroll
-  for (int j = 0; j < C::LOADS; ++j) {
-    const int slot = (j * C::WAVES + wave) * 64 + lane;
-    const int r = slot / C::CPR, s = slot % C::CPR;
-    const int ck = swz_k<C::CPR>(r, s), cv = swz_v<C::CPR>(r, s);
-    ok[j] = 8 * ck < a.D ? r * ks2 + ck * 16 : kNowhere;
-    ov[j] = 8 * cv < a.D ? r * vs2 + cv * 16 : kNowhere;
-  }
-  const uint16_t *kb = a.k + (int64_t)kvh * a.D, *vb = a.v + (int64_t)kvh * a.D;
-  auto issue = [&](int buf, int st) {
-    const int64_t key = (int64_t)t.key0 + (int64_t)st * C::KT;
-    const int left = min(t.keys - st * C::KT, C::KT);
-    const auto rk = rsrc(kb + key * a.k_stride,
-                         (uint32_t)(left - 1) * ks2 + 2 * a.D);
-    const auto rv = rsrc(vb + key * a.v_stride,
-                         (uint32_t)(left - 1) * vs2 + 2 * a.D);
-    char *base = smem + buf * C::STAGE + wave * 1024;
-#pragma unroll
-    for (int j = 0; j < C::LOADS; ++j)
-      load_lds16(rk, ok[j], base + j * C::WAVES * 1024);
-#pragma unroll
-    for (int j = 0; j < C::LOADS; ++j)
-      load_lds16(rv, ov[j], base + C::SIDE + j * C::WAVES * 1024);
-  };
-
-  // Fragments of K: key (lane & 31) of a score tile, 8 values a step.
-  int ak[C::KS];
-  {
+  // `wk`: which of the stage's keys are this wave's.
+  __device__ __forceinline__ void places(int lane, int wk) {
+    const int half = lane >> 5;
+    // Key (lane & 31) of a score tile.  The swizzle is an exclusive or, so an
+    // odd step's place is one bit off the even one's.
     const int r = lane & 31;
 #pragma unroll
-    for (int s = 0; s < C::KS; ++s)
-      ak[s] = (wk * C::KW + r) * C::RB + swz_k<C::CPR>(r, 2 * s + half) * 16;
-  }
-  // Fragments of V^T: of 16 keys a lane needs those that its scores stand for
-  // (4 half .. + 3 and 8 further), of value (lane & 31) of an output tile; a
-  // transposing read gives 16 lanes 4 keys of 16 values.
-  int av[C::NO];
-  {
-    const int i = lane & 15, r = 4 * half + i / 4;
+    for (int s = 0; s < C::KS / 2; ++s)
+      ak[s] = (wk * C::KW + r) * C::RB + swz_k<C::CPR>(r, 4 * s + half) * 16;
+    // Of 16 keys a lane needs those that its scores stand for (4 half .. + 3 and
+    // 8 further), of value (lane & 31) of an output tile; a transposing read
+    // gives 16 lanes 4 keys of 16 values.
+    const int i = lane & 15, rv = 4 * half + i / 4;
 #pragma unroll
     for (int n = 0; n < C::NO; ++n) {
       const int c = 4 * n + 2 * ((lane >> 4) & 1) + (i & 3) / 2;
-      av[n] = C::SIDE + (wk * C::KW + r) * C::RB + swz_v<C::CPR>(r, c) * 16 +
+      av[n] = C::SIDE + (wk * C::KW + rv) * C::RB + swz_v<C::CPR>(rv, c) * 16 +
               (i & 1) * 8;
     }
   }
 
-  v16f o[C::NO];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int n = 0; n < C::NO; ++n)
+    for (int n = 0; n < C::NO; ++n)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
-  float m = -kInf, cm = 0.0f, l = 0.0f;
-  const float c = a.scale_log2;
+      for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
+    cm = l = 0.0f;
+    limit = -kInf;
+  }
 
-  if (st0 < st1) issue(0, st0);
-  wait_vmcnt<0>();
-  block_barrier();
-  for (int st = st0; st < st1; ++st) {
-    const int buf = (st - st0) & 1;
-    if (st + 1 < st1) issue(buf ^ 1, st + 1);
-    const char *base = smem + buf * C::STAGE;
-
+  // A stage at `base`; `left` keys of it, from this wave's first on, count.
+  __device__ __forceinline__ void step(const char *base, int left, float c,
+                                       int half) {
     v16f s[C::NS];
 #pragma unroll
-    for (int n = 0; n < C::NS; ++n) {
+    for (int n = 0; n < C::NS; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[n][e] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < C::KS; ++k) {
-        const v8bf fk = *reinterpret_cast<const v8bf *>(
-            base + ak[k] + n * 32 * C::RB);
-        s[n] = mfma(fk, fq[k], s[n]);
-      }
+    for (int k = 0; k < C::KS; ++k)
+#pragma unroll
+      for (int n = 0; n < C::NS; ++n)
+        s[n] = mfma(*reinterpret_cast<const v8bf *>(
+                        base + (ak[k / 2] ^ (k & 1) * 32) + n * 32 * C::RB),
+                    fq[k], s[n]);
+    // Fragments are read a few matrix instructions ahead.
+    __builtin_amdgcn_sched_group_barrier(0x100, C::AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < C::KS * C::NS - C::AHEAD; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(0x008, C::AHEAD, 0);
+    __builtin_amdgcn_sched_barrier(0);
     // Keys past the end (their rows of LDS are zeros, whatever memory holds).
-    const int left = t.keys - st * C::KT - wk * C::KW;
     if (left < C::KW) {
 #pragma unroll
       for (int n = 0; n < C::NS; ++n)
@@ -357,14 +358,13 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(AttnArgs a,
     for (int n = 0; n < C::NS; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][e]);
-    if (__any(fmaf(top, c, -cm) > kLag || (m == -kInf && top > m))) {
-      const float now = fmaxf(m, max_halves(top));
-      const float was = m;
-      m = now;
-      const float ncm = now == -kInf ? 0.0f : now * c;
-      const float f =
-          was == -kInf ? 0.0f : __builtin_amdgcn_exp2f(cm - ncm);
+    if (__any(top * c > limit)) {
+      const float now = max_halves(top) * c;
+      const bool unset = limit == -kInf;
+      const float ncm = unset ? (now == -kInf ? 0.0f : now) : fmaxf(cm, now);
+      const float f = unset ? 0.0f : __builtin_amdgcn_exp2f(cm - ncm);
       cm = ncm;
+      limit = unset && now == -kInf ? -kInf : ncm + kLag;
       l *= f;
 #pragma unroll
       for (int n = 0; n < C::NO; ++n)
@@ -398,10 +398,136 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(AttnArgs a,
                 read_turned(base + av[d] + (32 * n + 16 * j + 8 * x) * C::RB);
           o[d] = mfma(fv.f, __builtin_bit_cast(v8bf, p[n][j]), o[d]);
         }
+  }
+};
+
+constexpr int kNowhere = 0x7FFFFFF0;  // past every buffer: reads zeros
+
+// The stages of a tile's keys and values, asked for one after the other.
+template <class C>
+struct Stages {
+  int ok[C::LOADS], ov[C::LOADS];  // what lands in this thread's 16 bytes
+  int ks2, vs2, D2, wave;
+  uint64_t kat, vat;               // the next stage's first row,
+  int left;                        // and the keys from it on
+
+  __device__ __forceinline__ void places(const AttnArgs &a, int wave_,
+                                         int lane) {
+    wave = wave_;
+    ks2 = (int)(a.k_stride * 2);
+    vs2 = (int)(a.v_stride * 2);
+    D2 = 2 * a.D;
+#pragma unroll
+    for (int j = 0; j < C::LOADS; ++j) {
+      const int slot = (j * C::WAVES + wave) * 64 + lane;
+      const int r = slot / C::CPR, s = slot % C::CPR;
+      const int ck = swz_k<C::CPR>(r, s), cv = swz_v<C::CPR>(r, s);
+      ok[j] = 16 * ck < D2 ? r * ks2 + ck * 16 : kNowhere;
+      ov[j] = 16 * cv < D2 ? r * vs2 + cv * 16 : kNowhere;
+    }
+  }
+
+  __device__ __forceinline__ void begin(const AttnArgs &a, int kvh, int key0,
+                                        int keys, int stage) {
+    const int64_t key = (int64_t)key0 + (int64_t)stage * C::KT;
+    kat = uniform64(reinterpret_cast<uint64_t>(
+        a.k + (int64_t)kvh * a.D + key * a.k_stride));
+    vat = uniform64(reinterpret_cast<uint64_t>(
+        a.v + (int64_t)kvh * a.D + key * a.v_stride));
+    left = keys - stage * C::KT;
+  }
+
+  // Without keys the stage is zeros and nothing is read.
+  __device__ __forceinline__ void ask(char *to) {
+    const int n = min(left, C::KT) - 1;
+    const v4u rk = rsrc(kat, n < 0 ? 0 : n * ks2 + D2);
+    const v4u rv = rsrc(vat, n < 0 ? 0 : n * vs2 + D2);
+    const uint32_t at = lds_at(to + wave * 1024);
+#pragma unroll
+    for (int j = 0; j < C::LOADS; ++j)
+      if ((j * C::WAVES + wave) * 1024 < C::SIDE)
+        load_lds16(rk, ok[j], at + j * C::WAVES * 1024);
+#pragma unroll
+    for (int j = 0; j < C::LOADS; ++j)
+      if ((j * C::WAVES + wave) * 1024 < C::SIDE)
+        load_lds16(rv, ov[j], at + C::SIDE + j * C::WAVES * 1024);
+    kat += (uint64_t)C::KT * ks2;
+    vat += (uint64_t)C::KT * vs2;
+    left -= C::KT;
+  }
+};
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
+    AttnArgs a, uint32_t per_head, int splits) {
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wq = wave / C::WK, wk = wave % C::WK;
+  const int half = lane >> 5;
+
+  // Work groups of one head run on one XCD, whose L2 then holds its keys.
+  const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int kvh = id / per_head;
+  uint32_t tile = id - kvh * per_head;
+  int split = 0;
+  if (splits > 1) {
+    split = tile % (uint32_t)splits;
+    tile /= (uint32_t)splits;
+  }
+  const Tile t = find_tile<C::TM>(a, tile);
+  if (t.nq == 0) return;
+  const int G = a.G;
+  const int rows = min(t.nq * G - t.row0, C::TM);
+  const int stages_all = (t.keys + C::KT - 1) / C::KT;
+  int st0 = 0, st1 = stages_all;
+  if (splits > 1) {
+    // fewer than 2^24 stages and 2^7 parts: within 32 bits
+    st0 = (uint32_t)(split * stages_all) / (uint32_t)splits;
+    st1 = (uint32_t)((split + 1) * stages_all) / (uint32_t)splits;
+  }
+
+  const RowMap map(t, G);
+  auto token = [&](int r) { return map.tok0 + map.past(r); };
+  auto head = [&](int r) { return kvh * G + map.head(r, map.past(r)); };
+
+  Stages<C> ahead;
+  ahead.places(a, wave, lane);
+  ahead.begin(a, kvh, t.key0, t.keys, st0);
+  if (st0 < st1) ahead.ask(smem);
+
+  Rows<C> w;
+  {
+    const int r = min(wq * 32 + (lane & 31), rows - 1);
+    const uint16_t *q =
+        a.q + (int64_t)token(r) * a.q_stride + (int64_t)head(r) * a.D;
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+      const int d = 16 * s + 8 * half;
+      v4u v = {0, 0, 0, 0};
+      if (d < a.D) v = *reinterpret_cast<const v4u *>(q + d);
+      w.fq[s] = __builtin_bit_cast(v8bf, v);
+    }
+  }
+  w.places(lane, wk);
+  w.clear();
+  // Q is there before the loop: a wait for it within would be one for the
+  // stages on their way.
+#pragma unroll
+  for (int s = 0; s < C::KS; ++s) asm volatile("" : "+v"(w.fq[s]));
+  wait_vmcnt<0>();
+  block_barrier();
+  for (int st = st0; st < st1; ++st) {
+    const int buf = (st - st0) & 1;
+    if (st + 1 < st1) ahead.ask(smem + (buf ^ 1) * C::STAGE);
+    w.step(smem + buf * C::STAGE, t.keys - st * C::KT - wk * C::KW,
+           a.scale_log2, half);
     wait_vmcnt<0>();
     block_barrier();
   }
-  l = add_halves(l);
+  v16f(&o)[C::NO] = w.o;
+  const float cm = w.cm;
+  const float l = add_halves(w.l);
 
   // Join the waves that share rows, and bring O into rows: through LDS, which
   // no wave reads keys from any more.
@@ -465,9 +591,11 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(AttnArgs a,
                                  4 * half) = two;
       }
     __syncthreads();
-    const int per = a.D / 8;
-    for (int i = tid; i < rows * per; i += C::THREADS) {
-      const int r = i / per, d = 8 * (i - r * per);
+    const int per = a.D / 8, step = C::THREADS / per;
+    int r = tid / per;
+    const int d = 8 * (tid - r * per);
+    if (r >= step) r = rows;
+    for (; r < rows; r += step) {
       const v2u *src = reinterpret_cast<const v2u *>(lo + r * C::OROW + d);
       const v2u x = src[0], y = src[1];
       *reinterpret_cast<v4u *>(a.out + (int64_t)token(r) * a.out_stride +
@@ -489,9 +617,11 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(AttnArgs a,
       part_ml(a, splits, split)[at] = make_float2(top, sum);
     }
     __syncthreads();
-    const int per = a.D / 4;
-    for (int i = tid; i < rows * per; i += C::THREADS) {
-      const int r = i / per, d = 4 * (i - r * per);
+    const int per = a.D / 4, step = C::THREADS / per;
+    int r = tid / per;
+    const int d = 4 * (tid - r * per);
+    if (r >= step) r = rows;
+    for (; r < rows; r += step) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < C::WK; ++w) {
@@ -511,19 +641,206 @@ __global__ __launch_bounds__(C::THREADS) void attention_kernel(AttnArgs a,
   }
 }
 
+// Many rows, few keys: what a tile reads and writes besides its keys (Q and O)
+// takes as long as its products, so a work group walks over a run of tiles and
+// asks for the next one's Q and first stage during this one's.  Two work groups
+// a compute unit; Q waits in LDS, 32 rows a wave, which no other wave touches.
+typedef __attribute__((address_space(4))) const AttnArgs KernelArgs;
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void attention_stream_kernel(
+    AttnArgs a, uint32_t per_head, uint32_t tiles) {
+  constexpr int QROWS = 32 * C::RB;  // bytes of a wave's Q
+  constexpr int QLOADS = QROWS / 1024;
+  __shared__ __attribute__((aligned(
+      1024))) char smem[2 * C::STAGE + C::WAVES * QROWS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5;
+  char *const my_q = smem + 2 * C::STAGE + wave * QROWS;
+  const int G = a.G;
+
+  // The lane once more, where what follows from it is worked out on the spot:
+  // held over the loop it would take registers that the stages need.
+  auto local_lane = [&]() __attribute__((always_inline)) {
+    int v = lane;
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+
+  // A run of tiles, head after head; neighbours are on one XCD.
+  const uint32_t g = xcd_remap(blockIdx.x, gridDim.x);
+  const uint32_t per = tiles / gridDim.x, more = tiles % gridDim.x;
+  uint32_t tile = g * per + min(g, more);
+  const uint32_t end = tile + per + (g < more ? 1 : 0);
+
+  Stages<C> ahead;
+  ahead.places(a, wave, lane);
+  Rows<C> w;
+  w.places(lane, 0);
+  auto rows_of = [&](const Tile &t) {  // of this wave, 32 at most
+    return min(t.nq * G - t.row0 - wave * 32, 32);
+  };
+  // Bytes from the wave's first token's heads of key head kvh to the end of its
+  // last row.  A wave with fewer than 32 rows holds the end of its sequence, so
+  // a row past them lies a token further, past these bytes.
+  auto bytes_of = [&](const RowMap &map, int n, int stride) {
+    const int r0 = wave * 32;
+    return n <= 0 ? 0
+                  : (map.past(r0 + n - 1) - map.past(r0)) * stride * 2 +
+                        G * 2 * a.D;
+  };
+  const int q_stride = (int)a.q_stride, out_stride = (int)a.out_stride;
+  // Q's rows, past the last of them zeros.
+  auto ask_q = [&](const Tile &t, int kvh) __attribute__((always_inline)) {
+    const RowMap map(t, G);
+    const int r0 = wave * 32, lane = local_lane();
+    const uint32_t at = lds_at(my_q);
+    const int first = __builtin_amdgcn_readfirstlane(map.past(r0));
+    const v4u r = rsrc(uniform64(reinterpret_cast<uint64_t>(
+                           a.q + (int64_t)(map.tok0 + first) * q_stride +
+                           (int64_t)kvh * G * a.D)),
+                       __builtin_amdgcn_readfirstlane(
+                           bytes_of(map, rows_of(t), q_stride)));
+#pragma unroll
+    for (int j = 0; j < QLOADS; ++j) {
+      const int row = j * (64 / C::CPR) + lane / C::CPR;
+      const int c = swz_k<C::CPR>(row, lane % C::CPR);
+      const int past = map.past(r0 + row);
+      const int off = (past - first) * q_stride * 2 +
+                      map.head(r0 + row, past) * 2 * a.D + c * 16;
+      load_lds16(r, 8 * c < a.D ? off : kNowhere, at + j * 1024);
+    }
+  };
+  // Tile i and its key head.  What only this needs of the arguments is read
+  // again, not held: the loop over stages has no scalar registers to spare, and
+  // without them the scheduler gives up on it (each instruction then waits for
+  // the one before: a sixth of the time).
+  auto find = [&](uint32_t i, int &kvh) __attribute__((always_inline)) {
+    KernelArgs *again =
+        (KernelArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(again));
+    kvh = i / per_head;
+    return find_equal_tile<C::TM>(*again, i - kvh * per_head);
+  };
+
+  int kvh = 0, buf = 0;
+  Tile t = find(tile, kvh);
+  ahead.begin(a, kvh, t.key0, t.keys, 0);
+  ask_q(t, kvh);
+  ahead.ask(smem);
+  bool full = false;  // the last tile's stores may still be on their way
+  for (;;) {
+    // A full tile's rows left in QLOADS stores at least (1 KiB each), all of
+    // them behind the loads that are waited for here.
+    if (full)
+      wait_vmcnt<QLOADS>();
+    else
+      wait_vmcnt<0>();
+    block_barrier();
+    {
+      const int at = local_lane(), r = at & 31;
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s)
+        w.fq[s] = *reinterpret_cast<const v8bf *>(
+            my_q + r * C::RB + swz_k<C::CPR>(r, 2 * s + (at >> 5)) * 16);
+    }
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) asm volatile("" : "+v"(w.fq[s]));
+    w.clear();
+
+    const bool more_tiles = tile + 1 < end;
+    int next_kvh = kvh;
+    const Tile nt = find(more_tiles ? tile + 1 : tile, next_kvh);
+    // A tile without keys has one stage of zeros.
+    const int ns = max((t.keys + C::KT - 1) / C::KT, 1);
+    for (int st = 0;; ++st) {
+      const bool last = st + 1 == ns;
+      if (last) ahead.begin(a, next_kvh, nt.key0, nt.keys, 0);
+      if (!last || more_tiles) ahead.ask(smem + (buf ^ 1) * C::STAGE);
+      // Q of the next tile behind that: it has the rest of the stages to come.
+      const bool q_too = st == 0 && more_tiles;
+      if (q_too) ask_q(nt, next_kvh);
+      w.step(smem + buf * C::STAGE, t.keys - st * C::KT, a.scale_log2, half);
+      if (last) break;
+      if (q_too)
+        wait_vmcnt<QLOADS>();
+      else
+        wait_vmcnt<0>();
+      block_barrier();
+      buf ^= 1;
+    }
+    block_barrier();  // no wave reads this stage any more
+
+    // O into rows, through the wave's part of this stage, half the width at a
+    // time.
+    const float sum = add_halves(w.l);
+    // A row that no key has a finite score for is 0 / 0; one without keys is 0.
+    const float f = t.keys == 0 ? 0.0f : 1.0f / sum;
+    constexpr int PART = C::STAGE / C::WAVES;      // bytes
+    constexpr int ORB = PART / 32;                 // of a row
+    constexpr int TILES = ORB / 64;                // output tiles at a time
+    constexpr int OCPR = ORB / 16;
+    char *const my_o = smem + buf * C::STAGE + wave * PART;
+    const int lane = local_lane();
+    const int n = rows_of(t);
+    full = n == 32 && a.D == C::DL;
+    static_assert(TILES >= 1, "");
+    const RowMap map(t, G);
+    const int r0 = wave * 32;
+    const int first = __builtin_amdgcn_readfirstlane(map.past(r0));
+    const auto rows = out_rsrc(
+        uniform64(reinterpret_cast<uint64_t>(
+            a.out + (int64_t)(map.tok0 + first) * out_stride +
+            (int64_t)kvh * G * a.D)),
+        __builtin_amdgcn_readfirstlane(bytes_of(map, n, out_stride)));
+#pragma unroll
+    for (int at = 0; at < C::NO; at += TILES) {
+#pragma unroll
+      for (int i = 0; i < TILES && at + i < C::NO; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const v16f &v = w.o[at + i];
+          const int chunk = (4 * i + e / 4) ^ (lane & (OCPR - 1));
+          *reinterpret_cast<v2u *>(my_o + (lane & 31) * ORB + chunk * 16 +
+                                   half * 8) =
+              v2u{pack_bf16x2(v[e] * f, v[e + 1] * f),
+                  pack_bf16x2(v[e + 2] * f, v[e + 3] * f)};
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < PART / 1024; ++j) {
+        const int r = j * (64 / OCPR) + lane / OCPR, c = lane % OCPR;
+        const int d = 32 * at + 8 * c;
+        const v4u v = *reinterpret_cast<const v4u *>(
+            my_o + r * ORB + (c ^ (r & (OCPR - 1))) * 16);
+        const int past = map.past(r0 + r);
+        const int off = (past - first) * out_stride * 2 +
+                        map.head(r0 + r, past) * 2 * a.D + 2 * d;
+        store16(v, rows, d < a.D ? off : kNowhere);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    if (!more_tiles) return;
+    t = nt;
+    ++tile;
+    kvh = next_kvh;
+    buf ^= 1;
+  }
+}
+
 // Joins the parts of a split: a row's largest c m, its parts' sums and values
 // scaled to that.  A part without keys has l 0 and its O is not read.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
 
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(
-    AttnArgs a, int splits) {
-  const int64_t per_head = gridDim.x / a.Hk;
-  const int kvh = (int)(blockIdx.x / per_head);
-  Tile t;
-  if (!find_tile<kJoinRows>(a, blockIdx.x - kvh * per_head, t)) return;
-  const int G = a.Hq / a.Hk;
-  const int rows = min((int64_t)t.nq * G - t.row0, (int64_t)kJoinRows);
+    AttnArgs a, uint32_t per_head, int splits) {
+  const int kvh = blockIdx.x / per_head;
+  const Tile t = find_tile<kJoinRows>(a, blockIdx.x - kvh * per_head);
+  if (t.nq == 0) return;
+  const int G = a.G;
+  const int rows = min(t.nq * G - t.row0, kJoinRows);
   const int per = a.D / 4;
   for (int i = threadIdx.x; i < rows * per; i += kJoinThreads) {
     const int r = i / per, d = 4 * (i - r * per);
@@ -553,11 +870,27 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(
   }
 }
 
+enum Config : int { kFew = 0, kSome = 1, kStream = 2, kMany = 3 };
+constexpr int kTileRows[4] = {32, 64, 256, 256};
+
 template <class C>
 hipError_t launch_cfg(const AttnArgs &a, const AttnPlan &plan,
                       hipStream_t stream) {
   const unsigned blocks = (unsigned)(plan.tiles * a.Hk * plan.splits);
-  attention_kernel<C><<<blocks, C::THREADS, 0, stream>>>(a, plan.splits);
+  attention_kernel<C><<<blocks, C::THREADS, 0, stream>>>(
+      a, (uint32_t)(plan.tiles * plan.splits), plan.splits);
+  return hipGetLastError();
+}
+
+constexpr int kStreamGroups = 256;  // one on each compute unit
+
+template <class C>
+hipError_t launch_stream(const AttnArgs &a, const AttnPlan &plan,
+                         hipStream_t stream) {
+  const int64_t tiles = plan.tiles * a.Hk;
+  attention_stream_kernel<C>
+      <<<(unsigned)(tiles < kStreamGroups ? tiles : kStreamGroups), C::THREADS,
+         0, stream>>>(a, (uint32_t)plan.tiles, (uint32_t)tiles);
   return hipGetLastError();
 }
 
@@ -565,14 +898,13 @@ template <int DP>
 hipError_t launch_width(const AttnArgs &a, const AttnPlan &plan,
                         hipStream_t stream) {
   switch (plan.config) {
-    case 0: return launch_cfg<Cfg<1, 4, 128, DP>>(a, plan, stream);
-    case 1: return launch_cfg<Cfg<2, 4, 128, DP>>(a, plan, stream);
-    default:
-      return launch_cfg<Cfg<8, 1, DP == 32 ? 128 : 64, DP>>(a, plan, stream);
+    case kFew: return launch_cfg<Cfg<1, 4, 128, DP>>(a, plan, stream);
+    case kSome: return launch_cfg<Cfg<2, 4, 128, DP>>(a, plan, stream);
+    case kStream: return launch_stream<Cfg<8, 1, DP == 32 ? 128 : 64, DP>>(a, plan, stream);
+    default: return launch_cfg<Cfg<8, 1, 64, DP>>(a, plan, stream);
   }
 }
 
-constexpr int kTileRows[3] = {32, 64, 256};
 
 int64_t count_tiles(int64_t Tq, int64_t B, bool packed, int64_t G, int rows) {
   return packed ? Tq * G / rows + B : B * ((Tq / B * G + rows - 1) / rows);
@@ -585,7 +917,7 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   AttnPlan p{};
   const int64_t G = Hq / Hk;
   const int64_t rows = (Tq + B - 1) / B * G;  // of a sequence, on average
-  p.config = rows <= 32 ? 0 : rows <= 64 ? 1 : 2;
+  p.config = rows <= 32 ? kFew : rows <= 64 ? kSome : kMany;
   p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
   // Keys are split where the tiles leave compute units idle.
   const int64_t groups = p.tiles * Hk;
@@ -594,13 +926,17 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   if (splits > stages / 2) splits = stages / 2;
   if (splits > 64) splits = 64;
   p.splits = splits < 1 ? 1 : (int)splits;
-  if (p.splits > 1)
+  if (p.splits > 1) {
     p.workspace = (size_t)p.splits * Tq * Hq * (D * 4 + 8);
+  } else if (p.config == kMany && !packed && Tk / B <= 1024) {
+    p.config = kStream;
+    p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
+  }
   return p;
 }
 
 bool attention_launchable(const AttnPlan &plan, int64_t Hk) {
-  const int threads[3] = {256, 512, 512};
+  const int threads[4] = {256, 512, 512, 512};
   return plan.tiles * Hk * plan.splits <
          (int64_t(1) << 32) / threads[plan.config];
 }
@@ -616,7 +952,7 @@ hipError_t launch_attention(const AttnArgs &a, const AttnPlan &plan,
   const int64_t tiles =
       count_tiles(a.Tq, a.B, a.q_offsets != nullptr, a.Hq / a.Hk, kJoinRows);
   attention_join_kernel<<<(unsigned)(tiles * a.Hk), kJoinThreads, 0, stream>>>(
-      a, plan.splits);
+      a, (uint32_t)tiles, plan.splits);
   return hipGetLastError();
 }
 

@@ -59,6 +59,7 @@ struct AttnArgs {
   int Tq, Tk, B, Hq, Hk, D;
   float scale_log2;  // scale * log2(e)
   void *workspace;
+  int G;  // query heads that share a key head
 };
 
 // How a call is cut: queries (times the heads that share keys) a tile, tiles

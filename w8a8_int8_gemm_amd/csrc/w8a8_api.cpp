@@ -401,7 +401,8 @@ int validate_attention(const w8a8_attention_t *a, w8a8::AttnArgs *args,
       a->q_offsets, a->k_offsets, a->k_lens,
       (int)a->Tq,  (int)a->Tk,  (int)a->B, (int)a->q_heads,
       (int)a->k_heads, (int)a->D,
-      (float)(a->scale * 1.44269504088896340736), nullptr};
+      (float)(a->scale * 1.44269504088896340736), nullptr,
+      (int)(a->q_heads / a->k_heads)};
   return W8A8_OK;
 }
 
