@@ -17,6 +17,7 @@ LIB_PATH = PKG / "libw8a8.so"
 
 OUT_BF16, OUT_FP32, OUT_I32 = 0, 1, 2
 W8A8_OK = 0
+W8A8_ERR_WORKSPACE = 4
 STATUS = {
     0: "W8A8_OK", 1: "W8A8_ERR_NULL", 2: "W8A8_ERR_SHAPE",
     3: "W8A8_ERR_ALIGN", 4: "W8A8_ERR_WORKSPACE", 5: "W8A8_ERR_OUT_DTYPE",
@@ -861,49 +862,64 @@ def rope_table(positions, pairs, *, theta=10000.0, scaling="none", factor=1.0,
     return out
 
 
-def _head_rows(t, name, shape=None):
-    """t: bf16 [T, heads, D], the heads of a token behind each other, tokens at
-    any stride (a part of a fused output's columns) -> that stride."""
+def _head_rows(t, name, batch=False):
+    """t: bf16 [tokens, heads, width], or with `batch` also [sequences, tokens,
+    heads, width]; the heads of a token behind each other, tokens at any stride
+    (a part of a fused output's columns), sequences behind each other -> (all
+    tokens, their stride)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     size, step = t.shape, t.stride()
-    if t.dtype != torch.bfloat16 or len(size) != 3 or \
-            (size[2] > 1 and step[2] != 1) or \
-            (size[1] > 1 and step[1] != size[2]):
+    dims = len(size)
+    if (t.dtype != torch.bfloat16 or not (dims == 3 or batch and dims == 4) or
+            (step[-1] != 1 and size[-1] > 1) or
+            (step[-2] != size[-1] and size[-2] > 1)):
         raise ValueError(f"{name}: expected {torch.bfloat16} [tokens, heads, "
                          f"width] with the heads of a token behind each "
                          f"other, got {t.dtype} {tuple(size)} with strides "
                          f"{step}")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got "
-                         f"{tuple(size)}")
     _on_current_gpu(t, name)
-    return step[0] if size[0] > 1 else size[1] * size[2]
+    rows = size[-3]
+    if dims == 4 and size[0] > 1:
+        if rows == 1:
+            return size[0], step[0]
+        if step[0] != rows * step[1]:
+            raise ValueError(f"{name}: the batch's sequences must follow each "
+                             f"other, got strides {step}")
+        return size[0] * rows, step[1]
+    return rows, step[-3] if rows > 1 else size[-2] * size[-1]
 
 
 def _heads_arg(x, y, kind, weight, bias, eps, name):
-    """A w8a8_heads_t; the vectors must outlive the call."""
-    stride = _head_rows(x, name)
-    H, D = x.shape[1:]
-    y_stride = _head_rows(y, f"{name}'s output", x.shape)
-    bf16 = _torch().bfloat16
+    """A w8a8_heads_t; y: the output given, or None for a new tensor -> (the
+    argument, its output); the vectors must outlive the call."""
+    stride = _head_rows(x, name)[1]
+    _, H, D = size = x.shape
+    if y is None:
+        y = x.new_empty(size)
+        y_stride = H * D
+    else:
+        y_stride = _head_rows(y, f"{name}'s output")[1]
+        if y.shape != size:
+            raise ValueError(f"{name}'s output: expected shape {tuple(size)}, "
+                             f"got {tuple(y.shape)}")
     per_head, ptr = None, [None, None]
-    for i, (t, what) in enumerate(((weight, "weight"), (bias, "bias"))):
+    for i, t in enumerate((weight, bias)):
         if t is None:
             continue
         full = t.dim() == 2
         if full and H == 1:
             full = False
             t = t[0]
-        _need(t, bf16, 2 if full else 1, f"{name} {what}",
+        _need(t, x.dtype, 2 if full else 1, f"{name} {('weight', 'bias')[i]}",
               (H, D) if full else (D,))
         if per_head is not None and per_head != full:
             raise ValueError(f"{name}: weight and bias must both be [{D}] or "
                              f"both [{H}, {D}]")
         per_head, ptr[i] = full, t.data_ptr()
     return _Heads(x.data_ptr(), y.data_ptr(), H, stride, y_stride,
-                  _Norm(kind, eps, *ptr), bool(per_head))
+                  (kind, eps, *ptr), bool(per_head)), y
 
 
 def _table_args(M, table, row):
@@ -938,42 +954,34 @@ def head_norm_rope(q, k=None, *, norm="rms", q_weight=None, q_bias=None,
     i and i + pairs, or 2 i and 2 i + 1 (interleaved); row m is token m's, or
     row[m] (int32 [M]; outside the table: padding, zeros).  out: a tensor (a
     pair with k), which may be the inputs."""
-    torch = _torch()
     code = NORM_KINDS.get(norm)
     if code is None:
         raise ValueError(f"norm: expected one of {sorted(NORM_KINDS)}, got "
                          f"{norm!r}")
-    for t, name in ((q, "q"), (k, "k")):
-        if not isinstance(t, torch.Tensor) and (name == "q" or t is not None):
-            raise TypeError(f"{name} must be a torch.Tensor")
-    own_out = out is None
     if k is None:
         if k_weight is not None or k_bias is not None:
             raise ValueError("k_weight and k_bias need k")
-        outs = (torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-                if own_out else out,)
+        out_q, out_k = out, None
+    elif out is None:
+        out_q = out_k = None
+    elif len(out) != 2:
+        raise ValueError("out: expected a pair, for q and for k")
     else:
-        if own_out:
-            outs = tuple(torch.empty(t.shape, dtype=torch.bfloat16,
-                                     device=t.device) for t in (q, k))
-        else:
-            outs = tuple(out)
-            if len(outs) != 2:
-                raise ValueError("out: expected a pair, for q and for k")
-    sides = [_heads_arg(q, outs[0], code, q_weight, q_bias, eps, "q")]
+        out_q, out_k = out
+    side_q, out_q = _heads_arg(q, out_q, code, q_weight, q_bias, eps, "q")
     M, _, D = q.shape
+    side_k = None
     if k is not None:
-        sides.append(_heads_arg(k, outs[1], code, k_weight, k_bias, eps, "k"))
+        side_k, out_k = _heads_arg(k, out_k, code, k_weight, k_bias, eps, "k")
         if k.shape[0] != M or k.shape[2] != D:
             raise ValueError(f"q and k disagree: {tuple(q.shape)}, "
                              f"{tuple(k.shape)}")
     rot = _table_args(M, table, row)
     _check("w8a8_head_norm_rope", lib().w8a8_head_norm_rope(
-        sides[0], sides[1] if k is not None else None, M, D, *rot,
-        bool(interleaved), _stream(stream)))
-    if own_out:
-        _on_stream(stream, *outs)
-    return outs[0] if k is None else outs
+        side_q, side_k, M, D, *rot, bool(interleaved), _stream(stream)))
+    if out is None:
+        _on_stream(stream, out_q, out_k)
+    return out_q if k is None else (out_q, out_k)
 
 
 def rope(x, table, *, row=None, interleaved=False, out=None, stream=None):
@@ -985,62 +993,17 @@ def rope(x, table, *, row=None, interleaved=False, out=None, stream=None):
                           interleaved=interleaved, out=out, stream=stream)
 
 
-def _flat_batch(t, name):
-    """[B, L, heads, D] -> [B L, heads, D]; anything else as it is."""
-    if isinstance(t, _torch().Tensor) and t.dim() == 4:
-        if t.shape[0] > 1 and t.shape[1] > 1 and \
-                t.stride(0) != t.shape[1] * t.stride(1):
-            raise ValueError(f"{name}: the batch's sequences must follow each "
-                             f"other, got strides {t.stride()}")
-        if t.shape[1] == 1:
-            return t[:, 0]
-        return t.as_strided((t.shape[0] * t.shape[1], *t.shape[2:]),
-                            t.stride()[1:])
-    return t
-
-
-def _attention_arg(q, k, v, out, scale, q_offsets, k_offsets, k_lens):
-    torch = _torch()
-    B = None
-    if isinstance(q, torch.Tensor) and q.dim() == 4:
-        if q_offsets is not None or k_offsets is not None:
-            raise ValueError("offsets go with [tokens, heads, width]")
-        B = q.shape[0]
-        for t, name in ((k, "k"), (v, "v")):
-            if not isinstance(t, torch.Tensor) or t.dim() != 4 or \
-                    t.shape[0] != B:
-                raise ValueError(f"{name}: expected [{B}, tokens, heads, "
-                                 "width] like q")
-        if out.shape != q.shape:
-            raise ValueError(f"out: expected shape {tuple(q.shape)}, got "
-                             f"{tuple(out.shape)}")
-    q, k, v, out = (_flat_batch(t, n) for t, n in (
-        (q, "q"), (k, "k"), (v, "v"), (out, "out")))
-    strides = [_head_rows(q, "q"), _head_rows(k, "k"),
-               _head_rows(v, "v", k.shape), _head_rows(out, "out", q.shape)]
-    if k.shape[2] != q.shape[2]:
-        raise ValueError(f"q and k disagree on the head width: "
-                         f"{q.shape[2]}, {k.shape[2]}")
-    for t, name in ((q_offsets, "q_offsets"), (k_offsets, "k_offsets")):
-        if t is None:
-            continue
-        _need(t, torch.int32, 1, name)
-        if t.shape[0] < 2 or (B is not None and t.shape[0] != B + 1):
-            raise ValueError(f"{name}: expected "
-                             f"{'two or more' if B is None else B + 1} "
-                             f"offsets, got {t.shape[0]}")
-        B = t.shape[0] - 1
-    if k_lens is not None:
-        _need(k_lens, torch.int32, 1, "k_lens", None if B is None else (B,))
-        B = k_lens.shape[0]
-    B = 1 if B is None else B
-    D = q.shape[2]
-    if scale is None:
-        scale = 1 / math.sqrt(D) if D else 1.0
-    return _Attention(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *strides,
-        q.shape[0], k.shape[0], B, q.shape[1], k.shape[1], D, _ptr(q_offsets),
-        _ptr(k_offsets), _ptr(k_lens), scale)
+def _offsets_arg(t, B, name):
+    """Pointer of int32 [B + 1] offsets (B None: any number), and B."""
+    if t is None:
+        return None, B
+    _need(t, _torch().int32, 1, name)
+    n = t.shape[0]
+    if n < 2 or (B is not None and n != B + 1):
+        raise ValueError(f"{name}: expected "
+                         f"{'two or more' if B is None else B + 1} offsets, "
+                         f"got {n}")
+    return t.data_ptr(), n - 1
 
 
 def attention(q, k, v, *, scale=None, q_offsets=None, k_offsets=None,
@@ -1056,21 +1019,60 @@ def attention(q, k, v, *, scale=None, q_offsets=None, k_offsets=None,
     keys count.  Returns bf16 of q's shape; rows outside of all sequences are
     not written, those of a sequence without keys are zero.  workspace:
     attention_workspace_bytes of uint8, of this call alone while it runs."""
-    torch = _torch()
+    Tq, q_stride = _head_rows(q, "q", True)
+    Tk, k_stride = _head_rows(k, "k", True)
+    _, v_stride = _head_rows(v, "v", True)
+    size, k_size = q.shape, k.shape
+    Hq, D = size[-2:]
+    Hk = k_size[-2]
+    if v.shape != k_size:
+        raise ValueError(f"v: expected shape {tuple(k_size)}, got "
+                         f"{tuple(v.shape)}")
+    if k_size[-1] != D or len(k_size) != len(size):
+        raise ValueError(f"q and k disagree: {tuple(size)}, {tuple(k_size)}")
+    B = None
+    if len(size) == 4:
+        if q_offsets is not None or k_offsets is not None:
+            raise ValueError("offsets go with [tokens, heads, width]")
+        B = size[0]
+        if k_size[0] != B:
+            raise ValueError(f"q and k disagree: {tuple(size)}, "
+                             f"{tuple(k_size)}")
+    qo, B = _offsets_arg(q_offsets, B, "q_offsets")
+    ko, B = _offsets_arg(k_offsets, B, "k_offsets")
+    kl = None
+    if k_lens is not None:
+        _need(k_lens, _torch().int32, 1, "k_lens", None if B is None else (B,))
+        kl, B = k_lens.data_ptr(), k_lens.shape[0]
     own_out = out is None
     if own_out:
-        if not isinstance(q, torch.Tensor):
-            raise TypeError("q must be a torch.Tensor")
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    a = _attention_arg(q, k, v, out, scale, q_offsets, k_offsets, k_lens)
-    L = lib()
-    ws = _workspace(int(L.w8a8_attention_workspace_bytes(a)), q.device,
-                    workspace)
-    ws_len = 0 if ws is None else ws.numel() * ws.element_size()
-    _check("w8a8_attention", L.w8a8_attention(a, _ptr(ws), ws_len,
-                                              _stream(stream)))
-    _on_stream(stream, out if own_out else None,
-               ws if workspace is None else None)
+        out = q.new_empty(size)
+        out_stride = Hq * D
+    else:
+        _, out_stride = _head_rows(out, "out", True)
+        if out.shape != size:
+            raise ValueError(f"out: expected shape {tuple(size)}, got "
+                             f"{tuple(out.shape)}")
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    a = _Attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                   q_stride, k_stride, v_stride, out_stride, Tq, Tk,
+                   1 if B is None else B, Hq, Hk, D, qo, ko, kl, scale)
+    L, s = lib(), _stream(stream)
+    if workspace is None:
+        # Most calls need none, and asking costs as much as such a call's checks.
+        status = L.w8a8_attention(a, None, 0, s)
+        if status == W8A8_ERR_WORKSPACE:
+            ws = _workspace(int(L.w8a8_attention_workspace_bytes(a)), q.device)
+            status = L.w8a8_attention(a, ws.data_ptr(), ws.numel(), s)
+            _on_stream(stream, ws)
+    else:
+        ws = _workspace(0, q.device, workspace)
+        status = L.w8a8_attention(a, ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), s)
+    _check("w8a8_attention", status)
+    if own_out:
+        _on_stream(stream, out)
     return out
 
 

@@ -830,42 +830,57 @@ __global__ __launch_bounds__(C::THREADS, 2) void attention_stream_kernel(
 }
 
 // Joins the parts of a split: a row's largest c m, its parts' sums and values
-// scaled to that.  A part without keys has l 0 and its O is not read.
+// scaled to that.  A part without keys has l 0 and its O is not read.  A thread
+// takes 4 values of a row; few rows a work group, so that all parts of a call of
+// few rows are on their way at once.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 8;
+constexpr int kMaxSplits = 64;
 
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(
     AttnArgs a, uint32_t per_head, int splits) {
+  __shared__ float2 parts[kJoinRows][kMaxSplits];  // l and the factor of a part
   const int kvh = blockIdx.x / per_head;
   const Tile t = find_tile<kJoinRows>(a, blockIdx.x - kvh * per_head);
   if (t.nq == 0) return;
   const int G = a.G;
   const int rows = min(t.nq * G - t.row0, kJoinRows);
+  const RowMap map(t, G);
+  auto row_at = [&](int r) {
+    const int past = map.past(r);
+    return (int64_t)(map.tok0 + past) * a.Hq + kvh * G + map.head(r, past);
+  };
+  const int lane = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < rows; r += kJoinThreads / 64) {
+    float2 ml = make_float2(-kInf, 0.0f);
+    if (lane < splits) ml = part_ml(a, splits, lane)[row_at(r)];
+    float top = ml.y != 0.0f ? ml.x : -kInf;
+#pragma unroll
+    for (int s = 32; s > 0; s /= 2) top = fmaxf(top, __shfl_xor(top, s));
+    parts[r][lane] = make_float2(
+        ml.y, ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top));
+  }
+  __syncthreads();
   const int per = a.D / 4;
   for (int i = threadIdx.x; i < rows * per; i += kJoinThreads) {
     const int r = i / per, d = 4 * (i - r * per);
-    const int tok = t.q0 + (t.row0 + r) / G, hd = kvh * G + (t.row0 + r) % G;
-    const int64_t at = (int64_t)tok * a.Hq + hd;
-    float top = -kInf;
-    for (int s = 0; s < splits; ++s) {
-      const float2 ml = part_ml(a, splits, s)[at];
-      if (ml.y != 0.0f) top = fmaxf(top, ml.x);
-    }
+    const int64_t at = row_at(r);
     float sum = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) {
-      const float2 ml = part_ml(a, splits, s)[at];
-      if (ml.y == 0.0f) continue;
-      const float f = __builtin_amdgcn_exp2f(ml.x - top);
-      sum += ml.y * f;
-      const float4 x =
-          *reinterpret_cast<const float4 *>(part_o(a, s) + at * a.D + d);
-      v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z),
-                      fmaf(x.w, f, v.w));
+      const float2 p = parts[r][s];
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (p.x != 0.0f)
+        x = *reinterpret_cast<const float4 *>(part_o(a, s) + at * a.D + d);
+      sum = fmaf(p.x, p.y, sum);
+      v = make_float4(fmaf(x.x, p.y, v.x), fmaf(x.y, p.y, v.y),
+                      fmaf(x.z, p.y, v.z), fmaf(x.w, p.y, v.w));
     }
     const float f = t.keys == 0 ? 0.0f : 1.0f / sum;
-    *reinterpret_cast<v2u *>(a.out + (int64_t)tok * a.out_stride +
-                             (int64_t)hd * a.D + d) =
+    const int past = map.past(r);
+    *reinterpret_cast<v2u *>(a.out + (int64_t)(map.tok0 + past) * a.out_stride +
+                             (int64_t)(kvh * G + map.head(r, past)) * a.D + d) =
         v2u{pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f)};
   }
 }
@@ -919,13 +934,16 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   const int64_t rows = (Tq + B - 1) / B * G;  // of a sequence, on average
   p.config = rows <= 32 ? kFew : rows <= 64 ? kSome : kMany;
   p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
-  // Keys are split where the tiles leave compute units idle.
+  // Keys are split where the tiles leave compute units idle, into a part a unit.
+  // The join behind it costs as much as three or four stages (one query, 56
+  // heads: 512 keys 9.3 us whole, 10.3 in 4 parts; 2048 keys 26 and 17).
   const int64_t groups = p.tiles * Hk;
   const int64_t stages = (Tk / B + 127) / 128;
-  int64_t splits = groups >= 256 ? 1 : 512 / groups;
-  if (splits > stages / 2) splits = stages / 2;
-  if (splits > 64) splits = 64;
-  p.splits = splits < 1 ? 1 : (int)splits;
+  int64_t splits = groups >= 256 ? 1 : 256 / groups;
+  if (splits > stages) splits = stages;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  if (splits < 1 || stages - (stages + splits - 1) / splits < 4) splits = 1;
+  p.splits = (int)splits;
   if (p.splits > 1) {
     p.workspace = (size_t)p.splits * Tq * Hq * (D * 4 + 8);
   } else if (p.config == kMany && !packed && Tk / B <= 1024) {
