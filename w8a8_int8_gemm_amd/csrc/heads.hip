@@ -4,6 +4,8 @@
 //
 // Both are streams: the table writes 8 bytes a token and pair, the head norms
 // read and write every value once (4 bytes), and the table's row once a token.
+#include <type_traits>
+
 #include "heads.h"
 #include "internal.h"
 #include "w8a8.h"
@@ -38,35 +40,41 @@ __device__ __forceinline__ SinCos quarter_sincos(float t) {
 }
 
 constexpr int kTableThreads = 256;
-constexpr int kTablePer = 4;  // pairs a thread
+constexpr int kTablePer = 4;  // tokens a thread
 
 // Position times frequency in quarter turns, in 64 bits: at position 10^6 the
 // angle of the fastest pair is off by 2^-33 of a radian, where 32 bits would
 // leave 2^-4.  The nearest whole number of quarters picks the quadrant, what is
-// left has its own digits in 32 bits.
+// left has its own digits in 32 bits.  A thread keeps one pair, so that its
+// frequency is read once and nothing is divided for a token.
+// Bound by its operations as much as by its stores: 37503 tokens of 64 pairs
+// (19 MB) 7.7 us, without the stores 6.0.
+template <class Pos>
 __global__ __launch_bounds__(kTableThreads) void rope_table_kernel(RopeArgs a) {
-  const uint32_t P = a.pairs;
-  const int64_t total = a.T * P;
-  int64_t e = (int64_t)blockIdx.x * (kTableThreads * kTablePer) + threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < kTablePer; ++i, e += kTableThreads) {
-    if (e >= total) return;
-    const int64_t t = total <= 0xFFFFFFFFll ? (uint32_t)e / P : e / P;
-    const uint32_t p = (uint32_t)(e - t * P);
-    const int64_t at = t * a.axes + a.axis[p];
-    const double pos = a.pos_type == W8A8_POSITIONS_I32
-                           ? (double)static_cast<const int32_t *>(a.pos)[at]
-                           : (double)static_cast<const float *>(a.pos)[at];
-    const double turns = pos * a.quarters[p];
+  const int P = a.pairs, at_once = kTableThreads / P;
+  const int first = threadIdx.x / P, p = threadIdx.x - first * P;
+  if (first >= at_once) return;
+  const double quarters = a.quarters[p];
+  const Pos *pos = static_cast<const Pos *>(a.pos) + a.axis[p];
+  int64_t t = (int64_t)blockIdx.x * (at_once * kTablePer) + first;
+#pragma unroll 4
+  for (int i = 0; i < kTablePer; ++i, t += at_once) {
+    if (t >= a.T) return;
+    const double turns = (double)pos[t * a.axes] * quarters;
     const double whole = __builtin_rint(turns);
     const SinCos sc = quarter_sincos((float)(turns - whole));
-    // the quadrant: whole mod 4, exact in 64 bits at any size
-    const int quad = (int)(whole - 4.0 * __builtin_floor(whole * 0.25));
+    // The quadrant, whole mod 4.  No pair turns faster than one radian a
+    // position, so INT32 positions stay below 2^31 quarters; the others may lie
+    // anywhere.
+    const int quad = std::is_integral<Pos>::value
+                         ? (int)whole & 3
+                         : (int)(whole - 4.0 * __builtin_floor(whole * 0.25));
     float c = (quad & 1) ? sc.s : sc.c, s = (quad & 1) ? sc.c : sc.s;
-    if (quad == 1 || quad == 2) c = -c;
-    if (quad & 2) s = -s;
-    a.table[2 * t * P + p] = c * a.amplitude;
-    a.table[2 * t * P + P + p] = s * a.amplitude;
+    c = quad == 1 || quad == 2 ? -c : c;
+    s = quad & 2 ? -s : s;
+    float *to = a.table + 2 * t * P + p;
+    to[0] = c * a.amplitude;
+    to[P] = s * a.amplitude;
   }
 }
 
@@ -139,9 +147,17 @@ HeadShape head_shape(const HeadArgs &a) {
 // L lanes a head.  A wave owns one token's heads of one side: it asks for all
 // of them, then for the token's table row and the weights, and turns and stores
 // them one after the other.  Waves share nothing.
-template <int L, bool HALF>
-__global__ __launch_bounds__(256) void head_norm_kernel(HeadArgs a,
-                                                        HeadShape shape) {
+//
+// STREAM: values go past the caches.  Where they all fit the L2s (32 MB) the next
+// call finds them there (64 tokens of 112 heads 3.9 us, past the caches 4.2);
+// beyond that they would only push each other out (2000 tokens 25.6 us, through
+// the caches 31.2; 19077 196 and 215).
+//
+// Five waves a SIMD: more of them spill (7: 294 us), four leave memory waiting
+// (202).
+template <int L, bool HALF, bool STREAM>
+__global__ __launch_bounds__(256, 5) void head_norm_kernel(HeadArgs a,
+                                                           HeadShape shape) {
   constexpr int HEADS = 64 / L;  // a round's
   const int lane = threadIdx.x & 63;
   const int64_t wave =
@@ -170,9 +186,11 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadArgs a,
   for (int u = 0; u < kHeadPasses; ++u) {
     const int h = head0 + u * HEADS;
     raw[u] = v4u{0, 0, 0, 0};
-    if (u < passes && live && h < s.heads && !pad)
-      raw[u] = *reinterpret_cast<const v4u *>(s.x + m * s.x_stride +
-                                              (int64_t)h * a.D + 8 * sub);
+    if (u < passes && live && h < s.heads && !pad) {
+      const v4u *from = reinterpret_cast<const v4u *>(
+          s.x + m * s.x_stride + (int64_t)h * a.D + 8 * sub);
+      raw[u] = STREAM ? __builtin_nontemporal_load(from) : *from;
+    }
   }
 
   // Cosines and sines of this lane's values, and which of its halves turn at
@@ -222,6 +240,9 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadArgs a,
   // Partners lie in the same half of 4 values where pairs % 8 == 0, else in
   // the other one.
   const bool odd = (P & 4) != 0;
+  // Two halves of 64: the partners lie 8 lanes on in the row of 16, which a lane
+  // permutation reaches without a trip through LDS.
+  const bool across = L == 16 && P == 64;
 
   const float width = (float)a.D;
   F8 w, b;
@@ -278,7 +299,10 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadArgs a,
         for (int e = 0; e < 4; ++e) {
           const int i = 4 * h2 + e;
           const float mine = odd ? x.v[4 * (1 - h2) + e] : x.v[i];
-          const float o = __shfl(mine, from[h2]);
+          const float o =
+              across ? __int_as_float(__builtin_amdgcn_update_dpp(
+                           0, __float_as_int(mine), 0x128, 0xF, 0xF, true))
+                     : __shfl(mine, from[h2]);
           y.v[i] = turned[h2] ? fmaf(x.v[i], c.v[i], o * d.v[i]) : x.v[i];
         }
     } else {
@@ -291,27 +315,43 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadArgs a,
       // A padding token's zeros are written as such: NaN in a weight or bias
       // does not reach it.
       const v4u packed = pad ? v4u{0, 0, 0, 0} : pack8(y);
-      *reinterpret_cast<v4u *>(s.y + m * s.y_stride + (int64_t)h * a.D +
-                               8 * sub) = packed;
+      v4u *to = reinterpret_cast<v4u *>(s.y + m * s.y_stride +
+                                        (int64_t)h * a.D + 8 * sub);
+      if (STREAM)
+        __builtin_nontemporal_store(packed, to);
+      else
+        *to = packed;
     }
   }
 }
 
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
 template <int L>
 void launch_lanes(const HeadArgs &a, const HeadShape &s, unsigned blocks,
                   hipStream_t stream) {
-  if (a.interleaved || a.pairs == 0)
-    head_norm_kernel<L, false><<<blocks, 256, 0, stream>>>(a, s);
+  const bool half = !a.interleaved && a.pairs > 0;
+  const bool past =
+      4 * a.M * (a.side[0].heads + a.side[1].heads) * a.D > kStreamBytes;
+  if (half && past)
+    head_norm_kernel<L, true, true><<<blocks, 256, 0, stream>>>(a, s);
+  else if (half)
+    head_norm_kernel<L, true, false><<<blocks, 256, 0, stream>>>(a, s);
+  else if (past)
+    head_norm_kernel<L, false, true><<<blocks, 256, 0, stream>>>(a, s);
   else
-    head_norm_kernel<L, true><<<blocks, 256, 0, stream>>>(a, s);
+    head_norm_kernel<L, false, false><<<blocks, 256, 0, stream>>>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_rope_table(const RopeArgs &a, hipStream_t stream) {
-  const int64_t per = kTableThreads * kTablePer;
-  const int64_t blocks = (a.T * a.pairs + per - 1) / per;
-  rope_table_kernel<<<(unsigned)blocks, kTableThreads, 0, stream>>>(a);
+  const int64_t per = kTableThreads / a.pairs * kTablePer;
+  const unsigned blocks = (unsigned)((a.T + per - 1) / per);
+  if (a.pos_type == W8A8_POSITIONS_I32)
+    rope_table_kernel<int32_t><<<blocks, kTableThreads, 0, stream>>>(a);
+  else
+    rope_table_kernel<float><<<blocks, kTableThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
