@@ -129,18 +129,6 @@ __device__ __forceinline__ uint32_t lds_at(const char *l) {
   return v;
 }
 
-// The same for stores; what lies past the end is not written.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rsrc(uint64_t at,
-                                                           uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)at, 0, bytes,
-                                           0x00020000);
-}
-
-__device__ __forceinline__ void store16(v4u v, __amdgpu_buffer_rsrc_t r,
-                                        int voff) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 0);
-}
-
 // Of a block of 4 rows x 16 values (a lane's 8 bytes at `l`: 4 values of row
 // lane % 16 / 4), the lane's column: one value of each row.
 __device__ __forceinline__ v4s read_turned(const char *l) {
@@ -162,10 +150,8 @@ __device__ __forceinline__ int clamped(int v, int lo, int hi) {
   return min(max(v, lo), hi);
 }
 
-// `Args`: AttnArgs, held or read again.
-template <class Args>
-__device__ __forceinline__ Tile tile_of(Args &a, int b, int q0, int nq,
-                                        int row0) {
+__device__ __forceinline__ Tile tile_of(const AttnArgs &a, int b, int q0,
+                                        int nq, int row0) {
   int key0 = 0, keys = a.Tk;
   if (a.k_offsets) {
     key0 = clamped(a.k_offsets[b], 0, a.Tk);
@@ -178,25 +164,21 @@ __device__ __forceinline__ Tile tile_of(Args &a, int b, int q0, int nq,
   return Tile{q0, nq, key0, keys, row0};
 }
 
-// Tile `i` of sequences of equal lengths, TM rows each.
-template <int TM, class Args>
-__device__ __forceinline__ Tile find_equal_tile(Args &a, uint32_t i) {
-  uint32_t b = 0, nq = a.Tq;
-  if (a.B > 1) {
-    nq = (uint32_t)a.Tq / (uint32_t)a.B;
-    const uint32_t per = (nq * a.G + TM - 1) / TM;
-    b = i / per;
-    i -= b * per;
-  }
-  return tile_of(a, b, b * nq, nq, i * TM);
-}
-
-// Tile `i` of all sequences; nq 0 past the last.  Offsets are clamped to the
-// rows there are, so no content of theirs leads outside.
+// Tile `i` of all sequences, TM rows each; nq 0 past the last.  Offsets are
+// clamped to the rows there are, so no content of theirs leads outside.
 template <int TM>
 __device__ __forceinline__ Tile find_tile(const AttnArgs &a, uint32_t i) {
-  if (!a.q_offsets) return find_equal_tile<TM>(a, i);
   const int G = a.G;
+  if (!a.q_offsets) {
+    uint32_t b = 0, nq = a.Tq;
+    if (a.B > 1) {
+      nq = (uint32_t)a.Tq / (uint32_t)a.B;
+      const uint32_t per = (nq * G + TM - 1) / TM;
+      b = i / per;
+      i -= b * per;
+    }
+    return tile_of(a, b, b * nq, nq, i * TM);
+  }
   // 64 sequences at a time: their tile counts summed over the lanes.
   const int lane = threadIdx.x & 63;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
@@ -641,194 +623,6 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kerne
   }
 }
 
-// Many rows, few keys: what a tile reads and writes besides its keys (Q and O)
-// takes as long as its products, so a work group walks over a run of tiles and
-// asks for the next one's Q and first stage during this one's.  Two work groups
-// a compute unit; Q waits in LDS, 32 rows a wave, which no other wave touches.
-typedef __attribute__((address_space(4))) const AttnArgs KernelArgs;
-
-template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void attention_stream_kernel(
-    AttnArgs a, uint32_t per_head, uint32_t tiles) {
-  constexpr int QROWS = 32 * C::RB;  // bytes of a wave's Q
-  constexpr int QLOADS = QROWS / 1024;
-  __shared__ __attribute__((aligned(
-      1024))) char smem[2 * C::STAGE + C::WAVES * QROWS];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5;
-  char *const my_q = smem + 2 * C::STAGE + wave * QROWS;
-  const int G = a.G;
-
-  // The lane once more, where what follows from it is worked out on the spot:
-  // held over the loop it would take registers that the stages need.
-  auto local_lane = [&]() __attribute__((always_inline)) {
-    int v = lane;
-    asm volatile("" : "+v"(v));
-    return v;
-  };
-
-  // A run of tiles, head after head; neighbours are on one XCD.
-  const uint32_t g = xcd_remap(blockIdx.x, gridDim.x);
-  const uint32_t per = tiles / gridDim.x, more = tiles % gridDim.x;
-  uint32_t tile = g * per + min(g, more);
-  const uint32_t end = tile + per + (g < more ? 1 : 0);
-
-  Stages<C> ahead;
-  ahead.places(a, wave, lane);
-  Rows<C> w;
-  w.places(lane, 0);
-  auto rows_of = [&](const Tile &t) {  // of this wave, 32 at most
-    return min(t.nq * G - t.row0 - wave * 32, 32);
-  };
-  // Bytes from the wave's first token's heads of key head kvh to the end of its
-  // last row.  A wave with fewer than 32 rows holds the end of its sequence, so
-  // a row past them lies a token further, past these bytes.
-  auto bytes_of = [&](const RowMap &map, int n, int stride) {
-    const int r0 = wave * 32;
-    return n <= 0 ? 0
-                  : (map.past(r0 + n - 1) - map.past(r0)) * stride * 2 +
-                        G * 2 * a.D;
-  };
-  const int q_stride = (int)a.q_stride, out_stride = (int)a.out_stride;
-  // Q's rows, past the last of them zeros.
-  auto ask_q = [&](const Tile &t, int kvh) __attribute__((always_inline)) {
-    const RowMap map(t, G);
-    const int r0 = wave * 32, lane = local_lane();
-    const uint32_t at = lds_at(my_q);
-    const int first = __builtin_amdgcn_readfirstlane(map.past(r0));
-    const v4u r = rsrc(uniform64(reinterpret_cast<uint64_t>(
-                           a.q + (int64_t)(map.tok0 + first) * q_stride +
-                           (int64_t)kvh * G * a.D)),
-                       __builtin_amdgcn_readfirstlane(
-                           bytes_of(map, rows_of(t), q_stride)));
-#pragma unroll
-    for (int j = 0; j < QLOADS; ++j) {
-      const int row = j * (64 / C::CPR) + lane / C::CPR;
-      const int c = swz_k<C::CPR>(row, lane % C::CPR);
-      const int past = map.past(r0 + row);
-      const int off = (past - first) * q_stride * 2 +
-                      map.head(r0 + row, past) * 2 * a.D + c * 16;
-      load_lds16(r, 8 * c < a.D ? off : kNowhere, at + j * 1024);
-    }
-  };
-  // Tile i and its key head.  What only this needs of the arguments is read
-  // again, not held: the loop over stages has no scalar registers to spare, and
-  // without them the scheduler gives up on it (each instruction then waits for
-  // the one before: a sixth of the time).
-  auto find = [&](uint32_t i, int &kvh) __attribute__((always_inline)) {
-    KernelArgs *again =
-        (KernelArgs *)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+s"(again));
-    kvh = i / per_head;
-    return find_equal_tile<C::TM>(*again, i - kvh * per_head);
-  };
-
-  int kvh = 0, buf = 0;
-  Tile t = find(tile, kvh);
-  ahead.begin(a, kvh, t.key0, t.keys, 0);
-  ask_q(t, kvh);
-  ahead.ask(smem);
-  bool full = false;  // the last tile's stores may still be on their way
-  for (;;) {
-    // A full tile's rows left in QLOADS stores at least (1 KiB each), all of
-    // them behind the loads that are waited for here.
-    if (full)
-      wait_vmcnt<QLOADS>();
-    else
-      wait_vmcnt<0>();
-    block_barrier();
-    {
-      const int at = local_lane(), r = at & 31;
-#pragma unroll
-      for (int s = 0; s < C::KS; ++s)
-        w.fq[s] = *reinterpret_cast<const v8bf *>(
-            my_q + r * C::RB + swz_k<C::CPR>(r, 2 * s + (at >> 5)) * 16);
-    }
-#pragma unroll
-    for (int s = 0; s < C::KS; ++s) asm volatile("" : "+v"(w.fq[s]));
-    w.clear();
-
-    const bool more_tiles = tile + 1 < end;
-    int next_kvh = kvh;
-    const Tile nt = find(more_tiles ? tile + 1 : tile, next_kvh);
-    // A tile without keys has one stage of zeros.
-    const int ns = max((t.keys + C::KT - 1) / C::KT, 1);
-    for (int st = 0;; ++st) {
-      const bool last = st + 1 == ns;
-      if (last) ahead.begin(a, next_kvh, nt.key0, nt.keys, 0);
-      if (!last || more_tiles) ahead.ask(smem + (buf ^ 1) * C::STAGE);
-      // Q of the next tile behind that: it has the rest of the stages to come.
-      const bool q_too = st == 0 && more_tiles;
-      if (q_too) ask_q(nt, next_kvh);
-      w.step(smem + buf * C::STAGE, t.keys - st * C::KT, a.scale_log2, half);
-      if (last) break;
-      if (q_too)
-        wait_vmcnt<QLOADS>();
-      else
-        wait_vmcnt<0>();
-      block_barrier();
-      buf ^= 1;
-    }
-    block_barrier();  // no wave reads this stage any more
-
-    // O into rows, through the wave's part of this stage, half the width at a
-    // time.
-    const float sum = add_halves(w.l);
-    // A row that no key has a finite score for is 0 / 0; one without keys is 0.
-    const float f = t.keys == 0 ? 0.0f : 1.0f / sum;
-    constexpr int PART = C::STAGE / C::WAVES;      // bytes
-    constexpr int ORB = PART / 32;                 // of a row
-    constexpr int TILES = ORB / 64;                // output tiles at a time
-    constexpr int OCPR = ORB / 16;
-    char *const my_o = smem + buf * C::STAGE + wave * PART;
-    const int lane = local_lane();
-    const int n = rows_of(t);
-    full = n == 32 && a.D == C::DL;
-    static_assert(TILES >= 1, "");
-    const RowMap map(t, G);
-    const int r0 = wave * 32;
-    const int first = __builtin_amdgcn_readfirstlane(map.past(r0));
-    const auto rows = out_rsrc(
-        uniform64(reinterpret_cast<uint64_t>(
-            a.out + (int64_t)(map.tok0 + first) * out_stride +
-            (int64_t)kvh * G * a.D)),
-        __builtin_amdgcn_readfirstlane(bytes_of(map, n, out_stride)));
-#pragma unroll
-    for (int at = 0; at < C::NO; at += TILES) {
-#pragma unroll
-      for (int i = 0; i < TILES && at + i < C::NO; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const v16f &v = w.o[at + i];
-          const int chunk = (4 * i + e / 4) ^ (lane & (OCPR - 1));
-          *reinterpret_cast<v2u *>(my_o + (lane & 31) * ORB + chunk * 16 +
-                                   half * 8) =
-              v2u{pack_bf16x2(v[e] * f, v[e + 1] * f),
-                  pack_bf16x2(v[e + 2] * f, v[e + 3] * f)};
-        }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-      for (int j = 0; j < PART / 1024; ++j) {
-        const int r = j * (64 / OCPR) + lane / OCPR, c = lane % OCPR;
-        const int d = 32 * at + 8 * c;
-        const v4u v = *reinterpret_cast<const v4u *>(
-            my_o + r * ORB + (c ^ (r & (OCPR - 1))) * 16);
-        const int past = map.past(r0 + r);
-        const int off = (past - first) * out_stride * 2 +
-                        map.head(r0 + r, past) * 2 * a.D + 2 * d;
-        store16(v, rows, d < a.D ? off : kNowhere);
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
-    if (!more_tiles) return;
-    t = nt;
-    ++tile;
-    kvh = next_kvh;
-    buf ^= 1;
-  }
-}
-
 // Joins the parts of a split: a row's largest c m, its parts' sums and values
 // scaled to that.  A part without keys has l 0 and its O is not read.  A thread
 // takes 4 values of a row; few rows a work group, so that all parts of a call of
@@ -885,8 +679,9 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(
   }
 }
 
-enum Config : int { kFew = 0, kSome = 1, kStream = 2, kMany = 3 };
-constexpr int kTileRows[4] = {32, 64, 256, 256};
+enum Config : int { kFew, kSome, kMid, kMany };
+constexpr int kTileRows[4] = {32, 64, 128, 256};
+constexpr int kThreads[4] = {256, 512, 256, 512};
 
 template <class C>
 hipError_t launch_cfg(const AttnArgs &a, const AttnPlan &plan,
@@ -897,25 +692,13 @@ hipError_t launch_cfg(const AttnArgs &a, const AttnPlan &plan,
   return hipGetLastError();
 }
 
-constexpr int kStreamGroups = 256;  // one on each compute unit
-
-template <class C>
-hipError_t launch_stream(const AttnArgs &a, const AttnPlan &plan,
-                         hipStream_t stream) {
-  const int64_t tiles = plan.tiles * a.Hk;
-  attention_stream_kernel<C>
-      <<<(unsigned)(tiles < kStreamGroups ? tiles : kStreamGroups), C::THREADS,
-         0, stream>>>(a, (uint32_t)plan.tiles, (uint32_t)tiles);
-  return hipGetLastError();
-}
-
 template <int DP>
 hipError_t launch_width(const AttnArgs &a, const AttnPlan &plan,
                         hipStream_t stream) {
   switch (plan.config) {
     case kFew: return launch_cfg<Cfg<1, 4, 128, DP>>(a, plan, stream);
     case kSome: return launch_cfg<Cfg<2, 4, 128, DP>>(a, plan, stream);
-    case kStream: return launch_stream<Cfg<8, 1, DP == 32 ? 128 : 64, DP>>(a, plan, stream);
+    case kMid: return launch_cfg<Cfg<4, 1, DP == 32 ? 128 : 64, DP>>(a, plan, stream);
     default: return launch_cfg<Cfg<8, 1, 64, DP>>(a, plan, stream);
   }
 }
@@ -932,31 +715,39 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   AttnPlan p{};
   const int64_t G = Hq / Hk;
   const int64_t rows = (Tq + B - 1) / B * G;  // of a sequence, on average
-  p.config = rows <= 32 ? kFew : rows <= 64 ? kSome : kMany;
+  const int64_t keys = Tk / B;
+  // Tiles of 256 rows (kMany) share a stage of keys among the most rows.  With
+  // few keys two work groups of 128 rows a compute unit do better: one's loads of
+  // Q and stores of O go on beside the other's products (19077 tokens, 56 heads:
+  // to 512 keys 353 us beside 386, to 1000 606 beside 633, to 2000 1104 beside
+  // 1121; 4096 to 4096, 42 heads 376 beside 358).  Where tiles of 256 are fewer
+  // than a quarter of the compute units, tiles of 64 rows, whose waves split a
+  // stage's keys (8 heads, 300 queries to 8192 keys 25 us beside 31; 56 heads, 300
+  // to 300, 112 tiles: 19 beside 14).
+  const int64_t large = count_tiles(Tq, B, packed, G, kTileRows[kMany]) * Hk;
+  p.config = rows <= 32                 ? kFew
+             : rows <= 64 || large < 64 ? kSome
+             : keys <= 2048             ? kMid
+                                        : kMany;
   p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
   // Keys are split where the tiles leave compute units idle, into a part a unit.
   // The join behind it costs as much as three or four stages (one query, 56
   // heads: 512 keys 9.3 us whole, 10.3 in 4 parts; 2048 keys 26 and 17).
   const int64_t groups = p.tiles * Hk;
-  const int64_t stages = (Tk / B + 127) / 128;
+  const int64_t stages = (keys + 127) / 128;
   int64_t splits = groups >= 256 ? 1 : 256 / groups;
   if (splits > stages) splits = stages;
   if (splits > kMaxSplits) splits = kMaxSplits;
   if (splits < 1 || stages - (stages + splits - 1) / splits < 4) splits = 1;
   p.splits = (int)splits;
-  if (p.splits > 1) {
+  if (p.splits > 1)
     p.workspace = (size_t)p.splits * Tq * Hq * (D * 4 + 8);
-  } else if (p.config == kMany && !packed && Tk / B <= 1024) {
-    p.config = kStream;
-    p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
-  }
   return p;
 }
 
 bool attention_launchable(const AttnPlan &plan, int64_t Hk) {
-  const int threads[4] = {256, 512, 512, 512};
   return plan.tiles * Hk * plan.splits <
-         (int64_t(1) << 32) / threads[plan.config];
+         (int64_t(1) << 32) / kThreads[plan.config];
 }
 
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &plan,
