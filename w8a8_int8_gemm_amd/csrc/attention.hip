@@ -62,17 +62,17 @@ struct Cfg {
   static_assert(LDS <= 160 * 1024, "");
 };
 
-// Where chunk c of row r lies in its row: fragments are read by 8 lanes a cycle
-// from consecutive rows (K), or as pairs of chunks of 4 consecutive rows (V),
-// which must fall into different parts of 128 bytes.
+// Where chunk c of row r lies in its row.  LDS gives 256 bytes a cycle if their
+// places differ by 256: to 16 lanes a chunk of consecutive rows each (K), to 32
+// lanes half a chunk each, 4 chunks side by side of 4 rows (V).
 template <int CPR>
 __device__ __forceinline__ int swz_k(int r, int c) {
-  return CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & (CPR - 1));
+  return c ^ ((r / (16 / CPR)) & (CPR - 1));
 }
 
 template <int CPR>
 __device__ __forceinline__ int swz_v(int r, int c) {
-  return CPR == 4 ? c ^ (((r >> 1) & 1) * 2) : c ^ ((r & (CPR / 2 - 1)) * 2);
+  return c ^ ((r & 3) / (16 / CPR) * 4);
 }
 
 __device__ __forceinline__ int xcd_remap(int bid, int T) {
