@@ -478,8 +478,9 @@ int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
  * to binary32 (6 * 2^-24 of the amplitude off at most).  A position that is NaN or
  * Inf gives NaN.
  * Shape: 1 <= T <= 2^24 - 1; 1 <= axes <= 4, each with 1 or more pairs, 256 in
- * all.  theta finite and > 1, factor finite and >= 1, amplitude finite; for
- * YARN original finite and > 0, beta_fast and beta_slow finite and > 0.
+ * all.  theta finite and > 1, factor finite and >= 1 (and what NTK makes of them
+ * finite), amplitude finite in binary32; for YARN original finite and > 0,
+ * beta_fast and beta_slow finite and > 0.
  * Errors: NULL, SHAPE, ARG, ALIGN, ALIAS, DEVICE, HIP.
  */
 #define W8A8_ROPE_MAX_AXES 4
@@ -579,7 +580,8 @@ int w8a8_head_norm_rope(const w8a8_heads_t *q, const w8a8_heads_t *k,
  * Shape: 1 <= B <= 2^20; 1 <= Tq, Tk (0 <= Tk: k and v may then be NULL) and
  * T * heads < 2^31; 8 <= D <= 128, D % 8 == 0; q_heads a multiple of k_heads;
  * strides multiples of 8, heads * D or more and below 2^22; a launch of fewer
- * than 2^32 work-items.  0 < scale < Inf.
+ * than 2^32 work-items.  0 < scale < Inf, and scale * q k^T within the binary32
+ * range.
  * Errors: NULL, SHAPE, ARG (scale), ALIGN (q, k, v, out: 16 bytes), WORKSPACE,
  * ALIAS, DEVICE, HIP.
  */

@@ -110,6 +110,31 @@ def test_packed(q_len, k_len, Hq, Hk, D):
     check(q, k, v, n, **shift)
 
 
+@pytest.mark.parametrize("n", [63, 64, 65, 4096, 4097, 20000])
+def test_many_packed_sequences(n):
+    """Sequences of 0 to 3 queries and keys, and two long ones among them."""
+    g = torch.Generator().manual_seed(n)
+    q_len, k_len = (torch.randint(0, 4, (n,), generator=g) for _ in "qk")
+    q_len[n // 2], k_len[n // 2] = 300, 70
+    q_len[n - 1], k_len[n // 3] = 65, 200
+    qo, ko = (torch.cat([torch.zeros(1, dtype=torch.int64), t.cumsum(0)]).to(
+        "cuda", torch.int32) for t in (q_len, k_len))
+    q, k, v = inputs(int(q_len.sum()), int(k_len.sum()), 2, 1, 32, n)
+    got = B.attention(q, k, v, q_offsets=qo, k_offsets=ko)
+    # some sequences against 64 bits
+    spans = R.sequences(q.shape[0], k.shape[0], n, qo, ko)
+    picked = [0, 1, n // 3, n // 2, n - 2, n - 1] + [
+        int(i) for i in torch.randint(0, n, (30,), generator=g)]
+    want, bound, covered = R.attention(q, k, v, [spans[b] for b in picked])
+    R.check_bf16(got[covered], want[covered], bound[covered])
+    # all of them where every value is the same (3 * 2^-1, which the weights'
+    # roundings do not change: they are divided by their own sum)
+    v[:] = 1.5
+    got = B.attention(q, k, v, q_offsets=qo, k_offsets=ko)
+    keyed = torch.repeat_interleave(k_len > 0, q_len).cuda()
+    assert (got[keyed] == 1.5).all() and (got[~keyed] == 0).all()
+
+
 @pytest.mark.parametrize("Lq,Lk", [(1, 512), (70, 100), (300, 333)])
 @pytest.mark.parametrize("Hq,Hk,D", [(4, 4, 128), (6, 2, 64)])
 def test_padded_batch(Lq, Lk, Hq, Hk, D):

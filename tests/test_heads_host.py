@@ -68,6 +68,8 @@ def test_table_valid_calls_reach_the_device_check(kw):
     (dict(rope=rope(theta=1.0)), ARG), (dict(rope=rope(theta=math.nan)), ARG),
     (dict(rope=rope(theta=math.inf)), ARG),
     (dict(rope=rope(amplitude=math.nan)), ARG),
+    (dict(rope=rope(amplitude=1e39)), ARG),
+    (dict(rope=rope((2, 8), scaling=2, factor=1e160)), ARG),
     (dict(rope=rope(scaling=1, factor=0.5)), ARG),
     (dict(rope=rope(scaling=2, factor=math.inf)), ARG),
     (dict(rope=rope(**{**YARN, "original": 0.0})), ARG),

@@ -1068,6 +1068,7 @@ def attention(q, k, v, *, scale=None, q_offsets=None, k_offsets=None,
             _on_stream(stream, ws)
     else:
         ws = _workspace(0, q.device, workspace)
+        _on_current_gpu(ws, "workspace")
         status = L.w8a8_attention(a, ws.data_ptr(),
                                   ws.numel() * ws.element_size(), s)
     _check("w8a8_attention", status)

@@ -164,11 +164,15 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs &a, int b, int q0,
   return Tile{q0, nq, key0, keys, row0};
 }
 
-// Tile `i` of all sequences, TM rows each; nq 0 past the last.  Offsets are
+// Tile `i` of all sequences, TM rows each; nq 0 where there is none.  Offsets are
 // clamped to the rows there are, so no content of theirs leads outside.
+// Packed sequence b has the tiles from S(b) = floor(rows before it / TM) + b on:
+// up to S(b + 1) there are as many as it needs at least, and all of them below
+// rows / TM + B, without a sum over the sequences.  S rises with b, so 64 lanes
+// find a tile's sequence in as many steps as B has digits of 64.
 template <int TM>
 __device__ __forceinline__ Tile find_tile(const AttnArgs &a, uint32_t i) {
-  const int G = a.G;
+  const uint32_t G = a.G;
   if (!a.q_offsets) {
     uint32_t b = 0, nq = a.Tq;
     if (a.B > 1) {
@@ -179,33 +183,27 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs &a, uint32_t i) {
     }
     return tile_of(a, b, b * nq, nq, i * TM);
   }
-  // 64 sequences at a time: their tile counts summed over the lanes.
+  auto first_tile = [&](int b) {
+    return (uint32_t)clamped(a.q_offsets[b], 0, a.Tq) * G / TM + (uint32_t)b;
+  };
   const int lane = threadIdx.x & 63;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int b = b0 + lane;
-    int q0 = 0, nq = 0;
-    if (b < a.B) {
-      q0 = clamped(a.q_offsets[b], 0, a.Tq);
-      nq = clamped(a.q_offsets[b + 1], q0, a.Tq) - q0;
-    }
-    const int mine = ((uint32_t)(nq * G) + TM - 1) / TM;
-    int upto = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const int o = __shfl_up(upto, s);
-      if (lane >= s) upto += o;
-    }
-    const int total = __builtin_amdgcn_readlane(upto, 63);
-    if ((int)i < total) {
-      const int at = __builtin_ctzll(__ballot(upto > (int)i));
-      return tile_of(a, b0 + at, __builtin_amdgcn_readlane(q0, at),
-                     __builtin_amdgcn_readlane(nq, at),
-                     ((int)i - (__builtin_amdgcn_readlane(upto, at) -
-                                __builtin_amdgcn_readlane(mine, at))) * TM);
-    }
-    i -= total;
+  int lo = 0, len = a.B;
+  for (;;) {
+    const int step = (len + 63) / 64, b = lo + lane * step;
+    const uint64_t at_or_before =
+        __ballot(lane * step < len && first_tile(b) <= i);
+    const int n = __builtin_popcountll(at_or_before);
+    if (n == 0) return Tile{0, 0, 0, 0, 0};
+    lo += (n - 1) * step;
+    if (step == 1) break;
+    len = min(step, len - (n - 1) * step);
   }
-  return Tile{0, 0, 0, 0, 0};
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int q0 = clamped(a.q_offsets[lo], 0, a.Tq);
+  const int nq = clamped(a.q_offsets[lo + 1], q0, a.Tq) - q0;
+  const uint32_t row0 = (i - first_tile(lo)) * TM;
+  if (row0 >= nq * G) return Tile{0, 0, 0, 0, 0};
+  return tile_of(a, lo, q0, nq, row0);
 }
 
 // Row r of a tile (r below 2^9): its token and its head among the G that share
@@ -440,7 +438,8 @@ struct Stages {
 };
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
+__global__
+__launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
     AttnArgs a, uint32_t per_head, int splits) {
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -461,12 +460,12 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kerne
   if (t.nq == 0) return;
   const int G = a.G;
   const int rows = min(t.nq * G - t.row0, C::TM);
-  const int stages_all = (t.keys + C::KT - 1) / C::KT;
+  const int stages_all = ((uint32_t)t.keys + C::KT - 1) / C::KT;
   int st0 = 0, st1 = stages_all;
   if (splits > 1) {
-    // fewer than 2^24 stages and 2^7 parts: within 32 bits
-    st0 = (uint32_t)(split * stages_all) / (uint32_t)splits;
-    st1 = (uint32_t)((split + 1) * stages_all) / (uint32_t)splits;
+    // at most 2^25 stages and 2^6 parts: within 32 bits
+    st0 = (uint32_t)split * (uint32_t)stages_all / (uint32_t)splits;
+    st1 = (uint32_t)(split + 1) * (uint32_t)stages_all / (uint32_t)splits;
   }
 
   const RowMap map(t, G);
@@ -698,7 +697,7 @@ hipError_t launch_width(const AttnArgs &a, const AttnPlan &plan,
   switch (plan.config) {
     case kFew: return launch_cfg<Cfg<1, 4, 128, DP>>(a, plan, stream);
     case kSome: return launch_cfg<Cfg<2, 4, 128, DP>>(a, plan, stream);
-    case kMid: return launch_cfg<Cfg<4, 1, DP == 32 ? 128 : 64, DP>>(a, plan, stream);
+    case kMid: return launch_cfg<Cfg<4, 1, 64, DP>>(a, plan, stream);
     default: return launch_cfg<Cfg<8, 1, 64, DP>>(a, plan, stream);
   }
 }

@@ -347,12 +347,15 @@ int validate_heads(const w8a8_heads_t *h, int64_t M, int64_t D) {
   return aligned(h->x, 16) && aligned(h->y, 16) ? W8A8_OK : W8A8_ERR_ALIGN;
 }
 
+double ntk_theta(const w8a8_rope_t &r, int p) {
+  return p > 1 ? r.theta * std::pow(r.factor, (double)p / (p - 1)) : r.theta;
+}
+
 // Quarter turns a position of pair i of an axis of p pairs.
 double rope_quarters(const w8a8_rope_t &r, int p, int i) {
   const double pi = 3.14159265358979323846;
-  double theta = r.theta;
-  if (r.scaling == W8A8_ROPE_NTK && p > 1)
-    theta *= std::pow(r.factor, (double)p / (p - 1));
+  const double theta =
+      r.scaling == W8A8_ROPE_NTK ? ntk_theta(r, p) : r.theta;
   double f = std::pow(theta, -(double)i / p);
   if (r.scaling == W8A8_ROPE_LINEAR) f /= r.factor;
   if (r.scaling == W8A8_ROPE_YARN) {
@@ -772,10 +775,13 @@ int w8a8_rope_table(const void *positions, int position_type, int64_t T,
   const int how = rope->scaling;
   if (how < W8A8_ROPE_NONE || how > W8A8_ROPE_YARN ||
       !positive(rope->theta) || rope->theta <= 1 ||
-      !std::isfinite(rope->amplitude))
+      !std::isfinite((float)rope->amplitude))
     return W8A8_ERR_ARG;
   if (how != W8A8_ROPE_NONE && (!positive(rope->factor) || rope->factor < 1))
     return W8A8_ERR_ARG;
+  if (how == W8A8_ROPE_NTK)
+    for (int i = 0; i < rope->axes; ++i)
+      if (!positive(ntk_theta(*rope, rope->pairs[i]))) return W8A8_ERR_ARG;
   if (how == W8A8_ROPE_YARN &&
       (!positive(rope->original) || !positive(rope->beta_fast) ||
        !positive(rope->beta_slow)))
