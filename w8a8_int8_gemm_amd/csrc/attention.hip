@@ -14,6 +14,12 @@
 // rounded ones, so that each row's weights still sum to one.  m lags: it moves
 // (and O and l with it) only where a row's scores pass it by more than 2^8, so
 // p stays below 2^8 and the sums far inside binary32.
+//
+// Bound by power where there are many rows: 19077 tokens to themselves, 56 heads
+// of 128, 9.0-9.5 ms (1.10-1.16 PFLOP/s; the library's BF16 product of 8192^3
+// 1.16, of 16384^3 1.40; inputs of zeros 1.5).  By memory where few rows read many
+// keys: 64 queries to 37503 keys 221 us, 5.2 TB/s while it reads.  Small calls by
+// their chain of trips: one query to 512 keys 10.4 us.
 #include "heads.h"
 #include "internal.h"
 #include "w8a8.h"
@@ -49,13 +55,14 @@ struct Cfg {
   static constexpr int NO = DP / 32;             // output tiles
   static constexpr int SIDE = KT * RB;           // bytes of a stage's K (or V)
   static constexpr int STAGE = 2 * SIDE;
+  // 16-byte loads of K a thread and stage
   static constexpr int LOADS = (SIDE / 16 + THREADS - 1) / THREADS;
-                                                   // of K a thread and stage
   static constexpr int OROW = DP + 4;            // floats of a joined row
   static constexpr int JOIN = (WK > 1 ? WK * TM * OROW * 4 : TM * OROW * 2) +
                               2 * WK * TM * 4;
   static constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
-  // Work groups a compute unit holds (of waves a SIMD, of LDS).
+  // Work groups a compute unit has registers for, and how many fragments of K
+  // are read ahead of their products.
   static constexpr int GROUPS = WAVES == 4 ? 2 : 1;
   static constexpr int AHEAD = KS * NS < 4 ? 2 : 4;
   static constexpr int WAVES_PER_SIMD = GROUPS * WAVES / 4;
