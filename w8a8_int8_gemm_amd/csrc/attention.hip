@@ -311,6 +311,9 @@ struct Rows {
   // A stage at `base`; `left` keys of it, from this wave's first on, count.
   __device__ __forceinline__ void step(const char *base, int left, float c,
                                        int half) {
+    // Ahead of the other wave's powers on the same SIMD: 1% (8192 tokens, 32 heads
+    // of 128 917 us beside 926).
+    __builtin_amdgcn_s_setprio(1);
     v16f s[C::NS];
 #pragma unroll
     for (int n = 0; n < C::NS; ++n)
@@ -332,6 +335,7 @@ struct Rows {
     }
     __builtin_amdgcn_sched_group_barrier(0x008, C::AHEAD, 0);
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
     // Keys past the end (their rows of LDS are zeros, whatever memory holds).
     if (left < C::KW) {
 #pragma unroll
