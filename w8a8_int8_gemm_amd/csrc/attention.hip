@@ -58,8 +58,8 @@ struct Cfg {
   // 16-byte loads of K a thread and stage
   static constexpr int LOADS = (SIDE / 16 + THREADS - 1) / THREADS;
   static constexpr int OROW = DP + 4;            // floats of a joined row
-  static constexpr int JOIN = (WK > 1 ? WK * TM * OROW * 4 : TM * OROW * 2) +
-                              2 * WK * TM * 4;
+  static constexpr int JOIN =
+      WK > 1 ? WK * TM * OROW * 4 + 2 * WK * TM * 4 : TM * OROW * 2;
   static constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
   // Work groups a compute unit has registers for, and how many fragments of K
   // are read ahead of their products.
@@ -488,8 +488,30 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
   ahead.begin(a, kvh, t.key0, t.keys, st0);
   if (st0 < st1) ahead.ask(smem);
 
+  // Q comes in whole rows, through the place of the second stage, where it fits
+  // there; read as fragments, each of its lines would be asked for four times.
+  constexpr bool THROUGH = C::TM * C::RB <= C::STAGE;
   Rows<C> w;
-  {
+  if (THROUGH) {
+    constexpr int QLOADS =
+        (C::TM * C::RB / 16 + C::THREADS - 1) / C::THREADS;
+    const v4u rq = rsrc(uniform64(reinterpret_cast<uint64_t>(
+                            a.q + (int64_t)map.tok0 * a.q_stride +
+                            (int64_t)kvh * G * a.D)),
+                        0x70000000u);
+    const uint32_t at = lds_at(smem + C::STAGE + wave * 1024);
+    const int qs2 = (int)(a.q_stride * 2);
+#pragma unroll
+    for (int j = 0; j < QLOADS; ++j) {
+      const int slot = (j * C::WAVES + wave) * 64 + lane;
+      const int r = slot / C::CPR, ch = swz_k<C::CPR>(r, slot % C::CPR);
+      const int past = map.past(r);
+      const int off = past * qs2 + map.head(r, past) * 2 * a.D + ch * 16;
+      if ((j * C::WAVES + wave) * 1024 < C::TM * C::RB)
+        load_lds16(rq, r < rows && 8 * ch < a.D ? off : kNowhere,
+                   at + j * C::WAVES * 1024);
+    }
+  } else {
     const int r = min(wq * 32 + (lane & 31), rows - 1);
     const uint16_t *q =
         a.q + (int64_t)token(r) * a.q_stride + (int64_t)head(r) * a.D;
@@ -503,6 +525,16 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
   }
   w.places(lane, wk);
   w.clear();
+  if (THROUGH) {
+    wait_vmcnt<0>();
+    block_barrier();
+    const int r = wq * 32 + (lane & 31);
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s)
+      w.fq[s] = *reinterpret_cast<const v8bf *>(
+          smem + C::STAGE + r * C::RB +
+          swz_k<C::CPR>(r, 2 * s + half) * 16);
+  }
   // Q is there before the loop: a wait for it within would be one for the
   // stages on their way.
 #pragma unroll
@@ -523,28 +555,32 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
 
   // Join the waves that share rows, and bring O into rows: through LDS, which
   // no wave reads keys from any more.
-  float *ml = reinterpret_cast<float *>(
-      smem + C::JOIN - 2 * C::WK * C::TM * 4);  // [WK][TM] of c m, then of l
   const int my_row = wq * 32 + (lane & 31);
-  if (half == 0) {
-    ml[wk * C::TM + my_row] = cm;
-    ml[(C::WK + wk) * C::TM + my_row] = l;
-  }
-  __syncthreads();
-  float top = -kInf, sum = 0.0f, f = 1.0f;
+  float top = cm, sum = l, f = 1.0f;
+  if (C::WK > 1) {
+    float *ml = reinterpret_cast<float *>(
+        smem + C::JOIN - 2 * C::WK * C::TM * 4);  // [WK][TM] of c m, then of l
+    if (half == 0) {
+      ml[wk * C::TM + my_row] = cm;
+      ml[(C::WK + wk) * C::TM + my_row] = l;
+    }
+    __syncthreads();
+    top = -kInf;
+    sum = 0.0f;
 #pragma unroll
-  for (int w = 0; w < C::WK; ++w) {
-    const float lw = ml[(C::WK + w) * C::TM + my_row];
-    if (lw != 0.0f) top = fmaxf(top, ml[w * C::TM + my_row]);
-  }
+    for (int w = 0; w < C::WK; ++w) {
+      const float lw = ml[(C::WK + w) * C::TM + my_row];
+      if (lw != 0.0f) top = fmaxf(top, ml[w * C::TM + my_row]);
+    }
 #pragma unroll
-  for (int w = 0; w < C::WK; ++w) {
-    const float lw = ml[(C::WK + w) * C::TM + my_row];
-    const float fw =
-        lw == 0.0f ? 0.0f
-                   : __builtin_amdgcn_exp2f(ml[w * C::TM + my_row] - top);
-    if (w == wk) f = fw;
-    sum += lw * fw;
+    for (int w = 0; w < C::WK; ++w) {
+      const float lw = ml[(C::WK + w) * C::TM + my_row];
+      const float fw =
+          lw == 0.0f ? 0.0f
+                     : __builtin_amdgcn_exp2f(ml[w * C::TM + my_row] - top);
+      if (w == wk) f = fw;
+      sum += lw * fw;
+    }
   }
   const bool whole = splits == 1;
   // A row that no key has a finite score for is 0 / 0; one without keys is 0.
