@@ -338,6 +338,26 @@ def test_at_model_sizes():
             R.check_bf16(got[:, h:h + 1], want, bound)
 
 
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("Lq,Lk,Hq,Hk", [(1100, 70, 32, 32), (550, 333, 60, 20),
+                                         (2000, 1, 32, 32)])
+def test_many_tiles_of_few_keys(D, Lq, Lk, Hq, Hk):
+    """Batches with more tiles than the chip holds at once, and ragged keys."""
+    n = 4
+    g = gen(D + Lk)
+    q = rand(g, n, Lq, Hq, D, std=1.5)
+    k, v = rand(g, n, Lk, Hk, D, std=1.5), rand(g, n, Lk, Hk, D)
+    lens = ints([Lk, 0, max(Lk - 33, 1), Lk // 2])
+    got = B.attention(q, k, v, k_lens=lens).flatten(0, 1)
+    flat = [t.flatten(0, 1) for t in (q, k, v)]
+    spans = R.sequences(n * Lq, n * Lk, n, k_lens=lens)
+    G = Hq // Hk
+    for h in (0, Hk - 1):
+        one = [flat[0][:, h * G:(h + 1) * G]] + [t[:, h:h + 1] for t in flat[1:]]
+        want, bound, _ = R.attention(*one, spans)
+        R.check_bf16(got[:, h * G:(h + 1) * G], want, bound)
+
+
 def test_binding_refuses():
     q, k, v = inputs(6, 9, 4, 2, 64, 13)
     o = ints([0, 3, 6])

@@ -60,11 +60,17 @@ struct Cfg {
   static constexpr int OROW = DP + 4;            // floats of a joined row
   static constexpr int JOIN =
       WK > 1 ? WK * TM * OROW * 4 + 2 * WK * TM * 4 : TM * OROW * 2;
-  static constexpr int LDS = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
+  // Q comes in whole rows, behind the first stage, where it needs little more
+  // than the second one's place.
+  static constexpr int QSIZE = TM * RB;
+  static constexpr bool THROUGH = TM <= 128;
+  static constexpr int BUFS =
+      THROUGH && QSIZE > STAGE ? STAGE + QSIZE : 2 * STAGE;
+  static constexpr int LDS = BUFS > JOIN ? BUFS : JOIN;
   // Work groups a compute unit has registers for, and how many fragments of K
   // are read ahead of their products.
-  static constexpr int GROUPS = WAVES == 4 ? 2 : 1;
-  static constexpr int AHEAD = KS * NS < 4 ? 2 : 4;
+  static constexpr int GROUPS = WAVES == 8 ? 1 : KT == 32 ? 3 : 2;
+  static constexpr int AHEAD = KS * NS < 4 ? 2 : GROUPS == 3 ? 3 : 4;
   static constexpr int WAVES_PER_SIMD = GROUPS * WAVES / 4;
   static_assert(LDS <= 160 * 1024, "");
 };
@@ -488,13 +494,10 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
   ahead.begin(a, kvh, t.key0, t.keys, st0);
   if (st0 < st1) ahead.ask(smem);
 
-  // Q comes in whole rows, through the place of the second stage, where it fits
-  // there; read as fragments, each of its lines would be asked for four times.
-  constexpr bool THROUGH = C::TM * C::RB <= C::STAGE;
+  // Read as fragments, each of Q's lines would be asked for four times.
   Rows<C> w;
-  if (THROUGH) {
-    constexpr int QLOADS =
-        (C::TM * C::RB / 16 + C::THREADS - 1) / C::THREADS;
+  if (C::THROUGH) {
+    constexpr int QLOADS = (C::QSIZE / 16 + C::THREADS - 1) / C::THREADS;
     const v4u rq = rsrc(uniform64(reinterpret_cast<uint64_t>(
                             a.q + (int64_t)map.tok0 * a.q_stride +
                             (int64_t)kvh * G * a.D)),
@@ -507,7 +510,7 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
       const int r = slot / C::CPR, ch = swz_k<C::CPR>(r, slot % C::CPR);
       const int past = map.past(r);
       const int off = past * qs2 + map.head(r, past) * 2 * a.D + ch * 16;
-      if ((j * C::WAVES + wave) * 1024 < C::TM * C::RB)
+      if ((j * C::WAVES + wave) * 1024 < C::QSIZE)
         load_lds16(rq, r < rows && 8 * ch < a.D ? off : kNowhere,
                    at + j * C::WAVES * 1024);
     }
@@ -525,7 +528,7 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
   }
   w.places(lane, wk);
   w.clear();
-  if (THROUGH) {
+  if (C::THROUGH) {
     wait_vmcnt<0>();
     block_barrier();
     const int r = wq * 32 + (lane & 31);
@@ -725,9 +728,9 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(
   }
 }
 
-enum Config : int { kFew, kSome, kMid, kMany };
-constexpr int kTileRows[4] = {32, 64, 128, 256};
-constexpr int kThreads[4] = {256, 512, 256, 512};
+enum Config : int { kFew, kSome, kMid, kShort, kMany };
+constexpr int kTileRows[5] = {32, 64, 128, 128, 256};
+constexpr int kThreads[5] = {256, 512, 256, 256, 512};
 
 template <class C>
 hipError_t launch_cfg(const AttnArgs &a, const AttnPlan &plan,
@@ -745,6 +748,7 @@ hipError_t launch_width(const AttnArgs &a, const AttnPlan &plan,
     case kFew: return launch_cfg<Cfg<1, 4, 128, DP>>(a, plan, stream);
     case kSome: return launch_cfg<Cfg<2, 4, 128, DP>>(a, plan, stream);
     case kMid: return launch_cfg<Cfg<4, 1, 64, DP>>(a, plan, stream);
+    case kShort: return launch_cfg<Cfg<4, 1, 32, DP>>(a, plan, stream);
     default: return launch_cfg<Cfg<8, 1, 64, DP>>(a, plan, stream);
   }
 }
@@ -763,18 +767,21 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   const int64_t rows = (Tq + B - 1) / B * G;  // of a sequence, on average
   const int64_t keys = Tk / B;
   // Tiles of 256 rows (kMany) share a stage of keys among the most rows.  With
-  // few keys two work groups of 128 rows a compute unit do better: one's loads of
-  // Q and stores of O go on beside the other's products (19077 tokens, 56 heads:
-  // to 512 keys 353 us beside 386, to 1000 606 beside 633, to 2000 1104 beside
-  // 1121; 4096 to 4096, 42 heads 376 beside 358).  Where tiles of 256 are fewer
-  // than a quarter of the compute units, tiles of 64 rows, whose waves split a
-  // stage's keys (8 heads, 300 queries to 8192 keys 25 us beside 31; 56 heads, 300
-  // to 300, 112 tiles: 19 beside 14).
+  // few keys two work groups of 128 rows a compute unit (kMid) do better: one's
+  // loads of Q and stores of O go on beside the other's products (19077 tokens, 56
+  // heads: to 512 keys 353 us beside 386, to 2000 1104 beside 1121; 4096 to 4096,
+  // 42 heads 376 beside 358); and where there are tiles for it, three with stages
+  // of 32 keys (kShort: 19077 to 77 keys 128 us beside 139, to 310 232 beside 243,
+  // to 1000 575 beside 581, to 2000 1133 beside 1104; 300 to 300, 12.4 beside
+  // 10.5).  Where tiles of 256 are fewer than a quarter of the compute units, tiles
+  // of 64 rows, whose waves split a stage's keys (kSome: 8 heads, 300 queries to
+  // 8192 keys 25 us beside 31; 56 heads, 300 to 300, 112 tiles: 19 beside 14).
   const int64_t large = count_tiles(Tq, B, packed, G, kTileRows[kMany]) * Hk;
-  p.config = rows <= 32                 ? kFew
-             : rows <= 64 || large < 64 ? kSome
-             : keys <= 2048             ? kMid
-                                        : kMany;
+  p.config = rows <= 32                    ? kFew
+             : rows <= 64 || large < 64    ? kSome
+             : keys > 2048                 ? kMany
+             : keys > 1024 || large <= 512 ? kMid
+                                           : kShort;
   p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
   // Keys are split where the tiles leave compute units idle, into a part a unit.
   // The join behind it costs as much as three or four stages (one query, 56
