@@ -153,8 +153,8 @@ HeadShape head_shape(const HeadArgs &a) {
 // beyond that they would only push each other out (2000 tokens 25.6 us, through
 // the caches 31.2; 19077 196 and 215).
 //
-// Five waves a SIMD: more of them spill (7: 294 us), four leave memory waiting
-// (202).
+// Told to leave room for five waves a SIMD the compiler keeps them without moving
+// its loads apart (196 us; untold 202, for six 202, for seven it spills: 294).
 template <int L, bool HALF, bool STREAM>
 __global__ __launch_bounds__(256, 5) void head_norm_kernel(HeadArgs a,
                                                            HeadShape shape) {
