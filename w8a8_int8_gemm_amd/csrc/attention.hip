@@ -103,6 +103,13 @@ __device__ __forceinline__ void wait_vmcnt() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// This wave's reads of LDS are done.  The builtin, which the compiler's own
+// counting of waits sees (vmcnt and expcnt stay unlimited: bits [15:14] and [3:0],
+// [6:4]; lgkmcnt 0: [11:8]).
+__device__ __forceinline__ void wait_lgkm() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+}
+
 // Barrier without the fences of __syncthreads, which would wait for direct
 // loads on their way; the waits are written out where they are due.
 __device__ __forceinline__ void block_barrier() {
@@ -552,6 +559,11 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
     if (st + 1 < st1) ahead.ask(smem + (buf ^ 1) * C::STAGE);
     w.step(smem + buf * C::STAGE, t.keys - st * C::KT - wk * C::KW,
            a.scale_log2, half);
+    // The reads of this stage are done (the compiler leaves its last products, and
+    // the waits for their operands, to behind the barrier, where another wave
+    // may fill the stage's place, or write its results over it), and the next
+    // stage has landed.
+    wait_lgkm();
     wait_vmcnt<0>();
     block_barrier();
   }
