@@ -257,7 +257,8 @@ class BlockHeads:
     int32 [M]) and the sequences (``binding.attention``'s offsets and key
     lengths; without them all tokens are one sequence, or ``batch`` equal ones).
     A padding token of the norms is a key like any other unless the offsets or
-    lengths leave it out."""
+    lengths leave it out.  Tokens of no sequence (offsets that do not cover all
+    of them) have an attention of zeros."""
     width: int
     norm: str = "rms"
     q_weight: object = None
@@ -344,6 +345,15 @@ class NormedBlock:
         rows = dict(mod_row=norms.mod_row, stream=stream)
         return run(x, projs, norms, rows, out, stream, context)
 
+    @staticmethod
+    def _zero(t, stream):
+        import torch
+        if stream is None:
+            t.zero_()
+            return
+        with torch.cuda.stream(stream):
+            t.zero_()
+
     def _attend(self, stream):
         """The attention of the block's Q, K, V outputs (queries and keys are
         normed and turned where they lie), or V's output without heads."""
@@ -362,6 +372,9 @@ class NormedBlock:
             B.head_norm_rope(q, out=q, **qv, **shared)
             B.head_norm_rope(k, q_weight=h.k_weight, q_bias=h.k_bias, out=k,
                              **shared)
+        if h.q_offsets is not None:
+            # Rows of no sequence, which the attention leaves as they are.
+            self._zero(self.a, stream)
         a = self.a.unflatten(1, (-1, h.width))
         if h.batch > 1 and h.q_offsets is None and h.k_offsets is None:
             q, k, v, a = (t.unflatten(0, (h.batch, -1)) for t in (q, k, v, a))
