@@ -881,6 +881,8 @@ def _head_rows(t, name, batch=False):
                          f"{step}")
     _on_current_gpu(t, name)
     rows = size[-3]
+    if rows == 0:  # nothing lies anywhere
+        return 0, size[-2] * size[-1]
     if dims == 4 and size[0] > 1:
         if rows == 1:
             return size[0], step[0]
