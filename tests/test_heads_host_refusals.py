@@ -6,6 +6,8 @@ import pytest
 import torch
 
 from w8a8_int8_gemm_amd import binding as B
+from w8a8_int8_gemm_amd import block as BL
+from w8a8_int8_gemm_amd import datagen as D
 
 BF = torch.bfloat16
 
@@ -25,3 +27,29 @@ def test_a_batch_without_rows(anywhere):
     # rows that do not follow each other are refused as before
     with pytest.raises(ValueError, match="follow each other"):
         B._head_rows(torch.zeros(3, 7, 2, 64, dtype=BF)[:, :5], "k", True)
+
+
+PROJS = (D.Proj("q", 0, 256, 128), D.Proj("k", 1, 128, 128),
+         D.Proj("v", 2, 128, 128), D.Proj("o", 3, 128, 256),
+         D.Proj("fc1", 4, 256, 128), D.Proj("fc2", 5, 128, 256))
+
+
+@pytest.mark.parametrize("kw,context,message", [
+    (dict(row=1), 9, "not turned"), (dict(row=1, table=1), 9, "not turned"),
+    (dict(table=1), 9, "not turned"), (dict(row=1), None, "needs a table"),
+    (dict(norm="none", q_weight=1), None, "need a norm"),
+    (dict(norm="none", k_weight=1, table=1), None, "need a norm"),
+    (dict(norm="none", k_bias=1), 9, "need a norm"),
+    (dict(norm="none", q_bias=1), 9, "need a norm")])
+def test_block_refuses_what_it_would_not_use(kw, context, message):
+    make = lambda heads: BL.NormedBlock(8, PROJS, device="cpu", heads=heads,
+                                        context_tokens=context)
+    with pytest.raises(ValueError, match=message):
+        make(BL.BlockHeads(64, **kw))
+    # also where they are set behind the block's construction
+    heads = BL.BlockHeads(64)
+    block = make(heads)
+    for name, value in kw.items():
+        setattr(heads, name, value)
+    with pytest.raises(ValueError, match=message):
+        block._attend(None)

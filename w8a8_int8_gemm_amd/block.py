@@ -275,6 +275,17 @@ class BlockHeads:
     k_offsets: object = None
     k_lens: object = None
 
+    def check(self, context: bool):
+        """Refuses what the block would not use."""
+        if context and (self.table is not None or self.row is not None):
+            raise ValueError("a context's keys are not turned")
+        if self.row is not None and self.table is None:
+            raise ValueError("row needs a table")
+        if self.norm == "none" and any(
+                t is not None for t in (self.q_weight, self.k_weight,
+                                        self.q_bias, self.k_bias)):
+            raise ValueError("weights and biases need a norm")
+
 
 class NormedBlock:
     """A whole block: norm and modulation, Q, K, V, the attention, its output
@@ -307,8 +318,7 @@ class NormedBlock:
             if context_tokens is not None:
                 raise ValueError("context_tokens needs heads")
         else:
-            if context_tokens is not None and heads.table is not None:
-                raise ValueError("a context's keys are not turned")
+            heads.check(context_tokens is not None)
             self.a = e(M, shape["q"][0])
             self.aws = e(max(B.attention_workspace_bytes(
                 M, Mk, shape["q"][0] // heads.width,
@@ -360,6 +370,7 @@ class NormedBlock:
         h = self.heads
         if h is None:
             return self.out["v"]
+        h.check(self.context_tokens is not None)
         q, k, v = (self.out[n].unflatten(1, (-1, h.width)) for n in "qkv")
         shared = dict(norm=h.norm, eps=h.eps, stream=stream)
         turn = dict(table=h.table, row=h.row, interleaved=h.interleaved)
