@@ -29,6 +29,28 @@ def test_a_batch_without_rows(anywhere):
         B._head_rows(torch.zeros(3, 7, 2, 64, dtype=BF)[:, :5], "k", True)
 
 
+@pytest.mark.parametrize("weight", [
+    torch.ones(5, 64, dtype=BF), torch.ones(2, 64, dtype=BF),
+    torch.ones(0, 64, dtype=BF), torch.ones(1, 64),
+    torch.ones(1, 128, dtype=BF)[:, ::2], torch.ones(1, 1, 64, dtype=BF)])
+@pytest.mark.parametrize("name", ["q_weight", "q_bias", "k_weight", "k_bias"])
+def test_vectors_of_one_head(anywhere, monkeypatch, name, weight):
+    """One head takes [1, width] or [width], and no vectors of other heads."""
+    x = torch.zeros(3, 1, 64, dtype=BF)
+    kw = dict(norm="layer", out=(x.clone(), x.clone()))
+    with pytest.raises(ValueError, match=name.replace("_", " ")):
+        B.head_norm_rope(x, x, **{name: weight}, **kw)
+    with pytest.raises(TypeError, match=name.replace("_", " ")):
+        B.head_norm_rope(x, x, **{name: [1.0] * 64}, **kw)
+    one = torch.ones(1, 64, dtype=BF)
+    for t in (one, one[0]):
+        arg, _ = B._heads_arg(x, None, 2, t, t, 1e-6, "q")
+        assert (arg.norm.weight, arg.per_head) == (t.data_ptr(), 0)
+    # [1, width] beside [width] stays allowed where they mean the same
+    arg, _ = B._heads_arg(x, None, 2, one, one[0], 1e-6, "q")
+    assert (arg.norm.weight, arg.norm.bias) == (one.data_ptr(),) * 2
+
+
 PROJS = (D.Proj("q", 0, 256, 128), D.Proj("k", 1, 128, 128),
          D.Proj("v", 2, 128, 128), D.Proj("o", 3, 128, 256),
          D.Proj("fc1", 4, 256, 128), D.Proj("fc2", 5, 128, 256))

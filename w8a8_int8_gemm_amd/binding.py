@@ -910,12 +910,10 @@ def _heads_arg(x, y, kind, weight, bias, eps, name):
     for i, t in enumerate((weight, bias)):
         if t is None:
             continue
-        full = t.dim() == 2
-        if full and H == 1:
-            full = False
-            t = t[0]
+        full = getattr(t, "ndim", 0) == 2
         _need(t, x.dtype, 2 if full else 1, f"{name} {('weight', 'bias')[i]}",
               (H, D) if full else (D,))
+        full = full and H > 1  # [1, D] is [D]
         if per_head is not None and per_head != full:
             raise ValueError(f"{name}: weight and bias must both be [{D}] or "
                              f"both [{H}, {D}]")
