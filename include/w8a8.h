@@ -580,8 +580,8 @@ int w8a8_head_norm_rope(const w8a8_heads_t *q, const w8a8_heads_t *k,
  * Shape: 1 <= B <= 2^20; 1 <= Tq, Tk (0 <= Tk: k and v may then be NULL) and
  * T * heads < 2^31; 8 <= D <= 128, D % 8 == 0; q_heads a multiple of k_heads;
  * strides multiples of 8, heads * D or more and below 2^22; a launch of fewer
- * than 2^32 work-items.  0 < scale < Inf, and scale * q k^T within the binary32
- * range.
+ * than 2^32 work-items.  0 < scale, and scale * log2(e) finite in binary32; the
+ * sums of q k^T, and scale * log2(e) times them, within the binary32 range.
  * Errors: NULL, SHAPE, ARG (scale), ALIGN (q, k, v, out: 16 bytes), WORKSPACE,
  * ALIAS, DEVICE, HIP.
  */

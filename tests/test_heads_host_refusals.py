@@ -5,6 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+from tests.test_heads_host import ARG, DEVICE, attend, no_gpu
 from w8a8_int8_gemm_amd import binding as B
 from w8a8_int8_gemm_amd import block as BL
 from w8a8_int8_gemm_amd import datagen as D
@@ -49,6 +50,21 @@ def test_vectors_of_one_head(anywhere, monkeypatch, name, weight):
     # [1, width] beside [width] stays allowed where they mean the same
     arg, _ = B._heads_arg(x, None, 2, one, one[0], 1e-6, "q")
     assert (arg.norm.weight, arg.norm.bias) == (one.data_ptr(),) * 2
+
+
+MOST = (2.0 - 2.0 ** -23) * 2.0 ** 127  # binary32's largest
+
+
+def test_scales_past_the_range_are_refused():
+    """The kernel multiplies scores by scale * log2(e)."""
+    for scale in (MOST, 2.0 ** 127.5, MOST / 1.4426):
+        assert attend(scale=scale) == ARG
+
+
+@no_gpu
+def test_scales_of_the_range_are_taken():
+    for scale in (MOST / 1.4428, 1.0, 2.0 ** -126, 2.0 ** -149):
+        assert attend(scale=scale) == DEVICE
 
 
 PROJS = (D.Proj("q", 0, 256, 128), D.Proj("k", 1, 128, 128),

@@ -10,10 +10,13 @@
 // product sums over keys in any order, so V's fragments are read (transposed,
 // from LDS) in the same order.
 //
-// Weights p = 2^(c s - c m) are rounded to BF16 for the matrix unit; l sums the
-// rounded ones, so that each row's weights still sum to one.  m lags: it moves
-// (and O and l with it) only where a row's scores pass it by more than 2^8, so
-// p stays below 2^8 and the sums far inside binary32.
+// Weights p = 2^(c s - c m) (c: scale log2 e) are rounded to BF16 for the matrix
+// unit; l sums the rounded ones, so that each row's weights still sum to one.  m
+// lags: it moves (and O and l with it) only where a row's scores pass it by more
+// than 2^8, so p stays near 2^8 at most and the sums far inside binary32.
+// c m is rounded, which costs a row's weights a common factor of up to
+// 2^(2^-24 |c m|); from |c m| = 2^31 on that would leave binary32.  So where |c m| is
+// large (kFar) the difference s - m is taken first.
 //
 // Bound by power where there are many rows: 19077 tokens to themselves, 56 heads
 // of 128, 9.0-9.5 ms (1.10-1.16 PFLOP/s; the library's BF16 product of 8192^3
@@ -40,6 +43,11 @@ constexpr float kInf = __builtin_inff();
 // How far scores may pass m, in powers of two: weights keep their relative
 // precision at any size, so it only has to stay far from the range's end.
 constexpr float kLag = 8.0f;
+// |c m| from which on weights are taken of s - m, in the branch that moves m, which
+// a wave with such a row then takes at every stage.  Below it c m is off by 2^-15 at
+// most, so weights of before and behind a move of m, or of waves and parts that
+// are joined, agree to 2^-15.
+constexpr float kFar = 1024.0f;
 
 // A tile of TM query rows and the keys of a stage.  WQ waves along the rows (32
 // each) times WK along the keys of a stage, whose results are joined at the
@@ -270,7 +278,7 @@ __device__ __forceinline__ float sum2(uint32_t p, float l) {
 }
 
 // Partial results of a split: per part and query row O (D values), then per
-// part and row c m and l.
+// part and row m and l.
 __device__ __forceinline__ float *part_o(const AttnArgs &a, int split) {
   return static_cast<float *>(a.workspace) +
          (int64_t)split * a.Tq * a.Hq * a.D;
@@ -291,8 +299,9 @@ struct Rows {
   int ak[C::KS / 2]; // places of the fragments of K and of V^T in a stage
   int av[C::NO];
   v16f o[C::NO];
-  // c m (0 until a score sets it), the c s that moves it, and l.
-  float cm, limit, l;
+  // m (0 until a score sets it), the score that moves it, and l.
+  float m, limit, l;
+  bool far;  // any of the wave's rows is
 
   // `wk`: which of the stage's keys are this wave's.
   __device__ __forceinline__ void places(int lane, int wk) {
@@ -320,8 +329,9 @@ struct Rows {
     for (int n = 0; n < C::NO; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
-    cm = l = 0.0f;
+    m = l = 0.0f;
     limit = -kInf;
+    far = false;
   }
 
   // A stage at `base`; `left` keys of it, from this wave's first on, count.
@@ -365,19 +375,26 @@ struct Rows {
     for (int n = 0; n < C::NS; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][e]);
-    if (__any(top * c > limit)) {
-      const float now = max_halves(top) * c;
+    if (far || __any(top > limit)) {
+      const float now = max_halves(top);
       const bool unset = limit == -kInf;
-      const float ncm = unset ? (now == -kInf ? 0.0f : now) : fmaxf(cm, now);
-      const float f = unset ? 0.0f : __builtin_amdgcn_exp2f(cm - ncm);
-      cm = ncm;
-      limit = unset && now == -kInf ? -kInf : ncm + kLag;
+      const float nm = unset ? (now == -kInf ? 0.0f : now) : fmaxf(m, now);
+      const float f = unset ? 0.0f : __builtin_amdgcn_exp2f((m - nm) * c);
+      m = nm;
+      limit = unset && now == -kInf ? -kInf : nm + kLag / c;
+      far = __any(fabsf(m * c) > kFar);
       l *= f;
 #pragma unroll
       for (int n = 0; n < C::NO; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[n][e] *= f;
+      const float sub = far ? m : 0.0f;
+#pragma unroll
+      for (int n = 0; n < C::NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[n][e] -= sub;
     }
+    const float cm = m * (far ? 0.0f : c);
     v4u p[C::NS][2];
 #pragma unroll
     for (int n = 0; n < C::NS; ++n)
@@ -568,18 +585,18 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
     block_barrier();
   }
   v16f(&o)[C::NO] = w.o;
-  const float cm = w.cm;
+  const float m = w.m, c = a.scale_log2;
   const float l = add_halves(w.l);
 
   // Join the waves that share rows, and bring O into rows: through LDS, which
   // no wave reads keys from any more.
   const int my_row = wq * 32 + (lane & 31);
-  float top = cm, sum = l, f = 1.0f;
+  float top = m, sum = l, f = 1.0f;
   if (C::WK > 1) {
     float *ml = reinterpret_cast<float *>(
-        smem + C::JOIN - 2 * C::WK * C::TM * 4);  // [WK][TM] of c m, then of l
+        smem + C::JOIN - 2 * C::WK * C::TM * 4);  // [WK][TM] of m, then of l
     if (half == 0) {
-      ml[wk * C::TM + my_row] = cm;
+      ml[wk * C::TM + my_row] = m;
       ml[(C::WK + wk) * C::TM + my_row] = l;
     }
     __syncthreads();
@@ -595,7 +612,7 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
       const float lw = ml[(C::WK + w) * C::TM + my_row];
       const float fw =
           lw == 0.0f ? 0.0f
-                     : __builtin_amdgcn_exp2f(ml[w * C::TM + my_row] - top);
+                     : __builtin_amdgcn_exp2f((ml[w * C::TM + my_row] - top) * c);
       if (w == wk) f = fw;
       sum += lw * fw;
     }
@@ -687,7 +704,7 @@ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void attention_kernel(
   }
 }
 
-// Joins the parts of a split: a row's largest c m, its parts' sums and values
+// Joins the parts of a split: a row's largest m, its parts' sums and values
 // scaled to that.  A part without keys has l 0 and its O is not read.  A thread
 // takes 4 values of a row; few rows a work group, so that all parts of a call of
 // few rows are on their way at once.
@@ -716,7 +733,9 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(
 #pragma unroll
     for (int s = 32; s > 0; s /= 2) top = fmaxf(top, __shfl_xor(top, s));
     parts[r][lane] = make_float2(
-        ml.y, ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top));
+        ml.y, ml.y == 0.0f
+                  ? 0.0f
+                  : __builtin_amdgcn_exp2f((ml.x - top) * a.scale_log2));
   }
   __syncthreads();
   const int per = a.D / 4;

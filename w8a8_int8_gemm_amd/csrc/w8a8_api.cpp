@@ -394,7 +394,8 @@ int validate_attention(const w8a8_attention_t *a, w8a8::AttnArgs *args,
       !stride_ok(a->out_stride, wq, limit) ||
       !stride_ok(a->k_stride, wk, limit) || !stride_ok(a->v_stride, wk, limit))
     return W8A8_ERR_SHAPE;
-  if (!(a->scale > 0) || !std::isfinite(a->scale)) return W8A8_ERR_ARG;
+  const float scale_log2 = (float)(a->scale * 1.44269504088896340736);
+  if (!(a->scale > 0) || !std::isfinite(scale_log2)) return W8A8_ERR_ARG;
   *plan = w8a8::plan_attention(a->Tq, a->Tk, a->B, a->q_offsets != nullptr,
                                a->q_heads, a->k_heads, a->D);
   if (!w8a8::attention_launchable(*plan, a->k_heads)) return W8A8_ERR_SHAPE;
@@ -404,7 +405,7 @@ int validate_attention(const w8a8_attention_t *a, w8a8::AttnArgs *args,
       a->q_offsets, a->k_offsets, a->k_lens,
       (int)a->Tq,  (int)a->Tk,  (int)a->B, (int)a->q_heads,
       (int)a->k_heads, (int)a->D,
-      (float)(a->scale * 1.44269504088896340736), nullptr,
+      scale_log2, nullptr,
       (int)(a->q_heads / a->k_heads)};
   return W8A8_OK;
 }
