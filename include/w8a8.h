@@ -473,9 +473,10 @@ int w8a8_w4_linear(const uint16_t *x, const uint8_t *w4,
  *           high = min(ceil(at(beta_slow)), 2 p - 1), at(b) = p *
  *           ln(original / (2 pi b)) / ln(theta); a high - low below 0.001
  *           counts as 0.001 ("YaRN", Peng et al., 2023)
- * and the table holds amplitude * cos and amplitude * sin.  Angles and
- * frequencies are taken in 64 bits (|angle| 2^-52 off), the result is rounded
- * to binary32 (6 * 2^-24 of the amplitude off at most).  A position that is NaN or
+ * and the table holds amplitude * cos and amplitude * sin.  Frequencies (off by
+ * 1.25 * 2^-52 of themselves at most) and their products with positions are rounded
+ * to binary64, so an angle is off by |angle| * 1.75 * 2^-52 at most; the result is
+ * rounded to binary32 (6 * 2^-24 of the amplitude off at most).  A position that is NaN or
  * Inf gives NaN.
  * Shape: 1 <= T <= 2^24 - 1; 1 <= axes <= 4, each with 1 or more pairs, 256 in
  * all.  theta finite and > 1, factor finite and >= 1 (and what NTK makes of them

@@ -27,7 +27,8 @@ SOURCES = ["w8a8_api.cpp", "rowwise.hip", "gemm.hip", "norm.hip", "w4.hip",
            "heads.hip", "attention.hip"]
 # Headers the library's sources include (part of its build id).
 HEADERS = [CSRC / "internal.h", CSRC / "rowwise.h",
-           CSRC / "norm.h", CSRC / "w4.h", CSRC / "heads.h", ROOT / "include" / "w8a8.h"]
+           CSRC / "norm.h", CSRC / "w4.h", CSRC / "heads.h", CSRC / "rope.h",
+           ROOT / "include" / "w8a8.h"]
 # Measurement support, not part of the library: the register-only MFMA
 # rate on given code matrices (loaded by bench.py only).
 CEILING_LIB = PKG / "libw8a8_ceiling.so"

@@ -15,6 +15,7 @@
 #include "heads.h"
 #include "internal.h"
 #include "norm.h"
+#include "rope.h"
 #include "rowwise.h"
 #include "w4.h"
 #include "w8a8.h"
@@ -345,30 +346,6 @@ int validate_heads(const w8a8_heads_t *h, int64_t M, int64_t D) {
   const int st = validate_norm(&h->norm);
   if (st != W8A8_OK) return st;
   return aligned(h->x, 16) && aligned(h->y, 16) ? W8A8_OK : W8A8_ERR_ALIGN;
-}
-
-double ntk_theta(const w8a8_rope_t &r, int p) {
-  return p > 1 ? r.theta * std::pow(r.factor, (double)p / (p - 1)) : r.theta;
-}
-
-// Quarter turns a position of pair i of an axis of p pairs.
-double rope_quarters(const w8a8_rope_t &r, int p, int i) {
-  const double pi = 3.14159265358979323846;
-  const double theta =
-      r.scaling == W8A8_ROPE_NTK ? ntk_theta(r, p) : r.theta;
-  double f = std::pow(theta, -(double)i / p);
-  if (r.scaling == W8A8_ROPE_LINEAR) f /= r.factor;
-  if (r.scaling == W8A8_ROPE_YARN) {
-    auto at = [&](double turns) {
-      return p * std::log(r.original / (2 * pi * turns)) / std::log(r.theta);
-    };
-    const double low = std::fmax(std::floor(at(r.beta_fast)), 0.0);
-    const double high = std::fmin(std::ceil(at(r.beta_slow)), 2.0 * p - 1);
-    const double span = std::fmax(high - low, 0.001);
-    const double ramp = std::fmin(std::fmax((i - low) / span, 0.0), 1.0);
-    f = f / r.factor * ramp + f * (1 - ramp);
-  }
-  return f * (2 / pi);
 }
 
 bool positive(double v) { return v > 0 && std::isfinite(v); }
@@ -782,7 +759,8 @@ int w8a8_rope_table(const void *positions, int position_type, int64_t T,
     return W8A8_ERR_ARG;
   if (how == W8A8_ROPE_NTK)
     for (int i = 0; i < rope->axes; ++i)
-      if (!positive(ntk_theta(*rope, rope->pairs[i]))) return W8A8_ERR_ARG;
+      if (!positive((double)w8a8::ntk_theta(*rope, rope->pairs[i])))
+        return W8A8_ERR_ARG;
   if (how == W8A8_ROPE_YARN &&
       (!positive(rope->original) || !positive(rope->beta_fast) ||
        !positive(rope->beta_slow)))
@@ -802,11 +780,10 @@ int w8a8_rope_table(const void *positions, int position_type, int64_t T,
   a.pairs = (int)pairs;
   a.amplitude = (float)rope->amplitude;
   int at = 0;
-  for (int x = 0; x < rope->axes; ++x)
-    for (int i = 0; i < rope->pairs[x]; ++i, ++at) {
-      a.axis[at] = (uint8_t)x;
-      a.quarters[at] = rope_quarters(*rope, rope->pairs[x], i);
-    }
+  for (int x = 0; x < rope->axes; at += rope->pairs[x++]) {
+    w8a8::rope_quarters(*rope, rope->pairs[x], a.quarters + at);
+    for (int i = 0; i < rope->pairs[x]; ++i) a.axis[at + i] = (uint8_t)x;
+  }
   return hip_status(
       w8a8::launch_rope_table(a, static_cast<hipStream_t>(stream)));
 }
