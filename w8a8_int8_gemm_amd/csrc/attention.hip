@@ -18,11 +18,13 @@
 // 2^(2^-24 |c m|); from |c m| = 2^31 on that would leave binary32.  So where |c m| is
 // large (kFar) the difference s - m is taken first.
 //
+// Times here and below are a call's GPU time in a captured graph whose calls take
+// three sets of inputs in turn, both sides of a comparison on one card.
 // Bound by power where there are many rows: 19077 tokens to themselves, 56 heads
-// of 128, 9.0-9.5 ms (1.10-1.16 PFLOP/s; the library's BF16 product of 8192^3
-// 1.16, of 16384^3 1.40; inputs of zeros 1.5).  By memory where few rows read many
-// keys: 64 queries to 37503 keys 221 us, 5.2 TB/s while it reads.  Small calls by
-// their chain of trips: one query to 512 keys 10.4 us.
+// of 128, 9.2 ms (1.13 PFLOP/s; 9.1 to 9.7 on other cards; the library's BF16
+// product of 8192^3 1.16, of 16384^3 1.40; inputs of zeros 1.5).  By memory where few
+// rows read many keys: 64 queries to 37503 keys 220 us, 5.0 TB/s while it reads.
+// Small calls by their chain of trips: one query to 512 keys 10.7 us.
 #include "heads.h"
 #include "internal.h"
 #include "w8a8.h"
@@ -78,8 +80,8 @@ struct Cfg {
       THROUGH && QSIZE > STAGE ? STAGE + QSIZE : 2 * STAGE;
   static constexpr int LDS = BUFS > JOIN ? BUFS : JOIN;
   // Work groups a compute unit has registers for, and how many fragments of K
-  // are read ahead of their products (4, 6 or 8: 988, 990, 993 us at 8192 tokens;
-  // 3 keep three work groups' registers).
+  // are read ahead of their products (4, 6 or 8: 965, 968, 972 us at 8192 tokens, 32
+  // heads of 128; 3 keep three work groups' registers).
   static constexpr int GROUPS = WAVES == 8 ? 1 : KT == 32 ? 3 : 2;
   static constexpr int AHEAD = KS * NS < 4 ? 2 : GROUPS == 3 ? 3 : 4;
   static constexpr int WAVES_PER_SIMD = GROUPS * WAVES / 4;
@@ -337,8 +339,8 @@ struct Rows {
   // A stage at `base`; `left` keys of it, from this wave's first on, count.
   __device__ __forceinline__ void step(const char *base, int left, float c,
                                        int half) {
-    // Ahead of the other wave's powers on the same SIMD: 1% (8192 tokens, 32 heads
-    // of 128 917 us beside 926).
+    // Ahead of the other wave's powers on the same SIMD: 0.3% (8192 tokens, 32 heads
+    // of 128 965 us beside 967-968).
     __builtin_amdgcn_s_setprio(1);
     v16f s[C::NS];
 #pragma unroll
@@ -801,17 +803,18 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   const int64_t rows = (Tq + B - 1) / B * G;  // of a sequence, on average
   const int64_t keys = Tk / B;
   // Up to 32 and 64 rows, the tile that holds them, so that keys are read once (64
-  // queries to 37503 keys: 217 us in one tile of 64 rows, 307 in two of 32).
+  // queries to 37503 keys: 221 us in one tile of 64 rows, 334 in two of 32).
   // Tiles of 256 rows (kMany) share a stage of keys among the most rows.  With
   // few keys two work groups of 128 rows a compute unit (kMid) do better: one's
   // loads of Q and stores of O go on beside the other's products (19077 tokens, 56
-  // heads: to 512 keys 353 us beside 386, to 2000 1104 beside 1121; 4096 to 4096,
-  // 42 heads 376 beside 358); and where there are tiles for it, three with stages
-  // of 32 keys (kShort: 19077 to 77 keys 128 us beside 139, to 310 232 beside 243,
-  // to 1000 575 beside 581, to 2000 1133 beside 1104; 300 to 300, 12.4 beside
-  // 10.5).  Where tiles of 256 are fewer than a quarter of the compute units, tiles
-  // of 64 rows, whose waves split a stage's keys (kSome: 8 heads, 300 queries to
-  // 8192 keys 25 us beside 31; 56 heads, 300 to 300, 112 tiles: 19 beside 14).
+  // heads of 128: to 512 keys 342 us beside 368, to 2000 1065 beside 1063; 4096 to
+  // 4096, 42 heads 373 beside 344); and where there are tiles for it, three with
+  // stages of 32 keys (kShort beside kMid: 19077 to 77 keys 147 us and 160, to 310 244
+  // and 252, to 1000 588 and 587, to 2000 1078 and 1065; 300 to 300, 13.5 and 11.2).
+  // Where tiles of 256 are fewer than a quarter of the compute units, tiles of 64
+  // rows, whose waves split a stage's keys (kSome beside kMany: 8 heads, 300 queries
+  // to 8192 keys 27 us and 32; 56 heads, 300 to 300, 112 tiles: 18 and 15).  All at
+  // width 128; no other width was measured.
   const int64_t large = count_tiles(Tq, B, packed, G, kTileRows[kMany]) * Hk;
   p.config = rows <= 32                    ? kFew
              : rows <= 64 || large < 64    ? kSome
@@ -821,7 +824,7 @@ AttnPlan plan_attention(int64_t Tq, int64_t Tk, int64_t B, bool packed,
   p.tiles = count_tiles(Tq, B, packed, G, kTileRows[p.config]);
   // Keys are split where the tiles leave compute units idle, into a part a unit.
   // The join behind it costs as much as three or four stages (one query, 56
-  // heads: 512 keys 9.3 us whole, 10.3 in 4 parts; 2048 keys 26 and 17).
+  // heads: 512 keys 10.6 us whole, 11.4 in 4 parts; 2048 keys 27 and 18).
   const int64_t groups = p.tiles * Hk;
   const int64_t stages = (keys + 127) / 128;
   int64_t splits = groups >= 256 ? 1 : 256 / groups;

@@ -4,6 +4,8 @@
 //
 // Both are streams: the table writes 8 bytes a token and pair, the head norms
 // read and write every value once (4 bytes), and the table's row once a token.
+// Times are a call's GPU time in a captured graph whose calls take three sets of
+// inputs in turn, both sides of a comparison on one card; 56 + 56 heads of 128.
 #include <type_traits>
 
 #include "heads.h"
@@ -48,7 +50,7 @@ constexpr int kTablePer = 4;  // tokens a thread
 // left has its own digits in 32 bits.  A thread keeps one pair, so that its
 // frequency is read once and nothing is divided for a token.
 // Bound by its operations as much as by its stores: 37503 tokens of 64 pairs
-// (19 MB) 7.7 us, without the stores 6.0.
+// (19 MB) 7.3 us, without the stores 6.0.
 template <class Pos>
 __global__ __launch_bounds__(kTableThreads) void rope_table_kernel(RopeArgs a) {
   const int P = a.pairs, at_once = kTableThreads / P;
@@ -134,8 +136,8 @@ HeadShape head_shape(const HeadArgs &a) {
   for (int i = 0; i < 2; ++i) {
     const int64_t rounds = ((int64_t)a.side[i].heads * s.lanes + 63) / 64;
     // A wave's table row and weights serve all its rounds, so many are better,
-    // as long as there are waves for every place on the chip (19077 tokens: 215
-    // us with up to 8 rounds, 218 with 4, 226 with 2; 14 spill).
+    // as long as there are waves for every place on the chip (19077 tokens: 208
+    // us with up to 8 rounds, 225 with 4, 251 with 2; 14 spill).
     int64_t most = a.M * rounds / 8192;
     most = most < 1 ? 1 : most > kHeadPasses ? kHeadPasses : most;
     const int64_t chunks = rounds ? (rounds + most - 1) / most : 0;
@@ -149,13 +151,14 @@ HeadShape head_shape(const HeadArgs &a) {
 // of them, then for the token's table row and the weights, and turns and stores
 // them one after the other.  Waves share nothing.
 //
-// STREAM: values go past the caches.  Where they all fit the L2s (32 MB) the next
-// call finds them there (64 tokens of 112 heads 3.9 us, past the caches 4.2);
-// beyond that they would only push each other out (2000 tokens 25.6 us, through
-// the caches 31.2; 19077 196 and 215).
+// STREAM: values go past the caches.  Where they all fit the L2s (32 MB) they stay
+// for the attention behind this (the norms themselves take as long either way: 64
+// tokens 3.6 us); beyond that they would only push each other out (2000 tokens 28
+// us, through the caches 30; 19077 208 and 225).
 //
 // Told to leave room for five waves a SIMD the compiler keeps them without moving
-// its loads apart (196 us; untold 202, for six 202, for seven it spills: 294).
+// its loads apart (19077 tokens 208 us; untold 213, for six 256, for seven it spills:
+// 354).
 template <int L, bool HALF, bool STREAM>
 __global__ __launch_bounds__(256, 5) void head_norm_kernel(HeadArgs a,
                                                            HeadShape shape) {
@@ -242,7 +245,8 @@ __global__ __launch_bounds__(256, 5) void head_norm_kernel(HeadArgs a,
   // the other one.
   const bool odd = (P & 4) != 0;
   // Two halves of 64: the partners lie 8 lanes on in the row of 16, which a lane
-  // permutation reaches without a trip through LDS (202 us beside 206).
+  // permutation reaches without a trip through LDS (19077 tokens 208 us either way:
+  // the trips are covered).
   const bool across = L == 16 && P == 64;
 
   const float width = (float)a.D;
